@@ -315,6 +315,27 @@ moe_status moe_forward(const moe_layer_desc* desc, int T, const moe_bf16* x, con
                        int32_t* counts_out, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * MoE.forward for a few tokens: the arguments, outputs and definitions of moe_forward, computed by one
+ * kernel launch for T <= MOE_DECODE_MAX_TOKENS (MOE_ERR_UNSUPPORTED above).  Made for decode batches,
+ * where moe_forward's seven launches and their gaps cost more than the arithmetic: the whole grid is
+ * resident and streams the chosen experts' weights without a break from the gate to the combine.
+ * Values: the same formulas with fp32 accumulation; h is rounded once to bf16 and, unlike
+ * moe_forward, the expert outputs stay in fp32 until the combine.  Results do not depend on scheduling.
+ * The selection may differ from moe_forward's where two experts' scores agree to fp32 rounding.
+ * A table row that names an expert twice counts it twice (in the weights, in y and in counts_out).
+ * desc->options, token_chunk and gate_prepared choose nothing here (they are still checked).
+ * The launch is cooperative: it starts when every SM it uses has room for its CTA, and it can be
+ * captured in a CUDA graph.  The workspace (moe_workspace_bytes(desc, T), initialised once) holds the
+ * grid's counters and rows, so calls that may run at the same time need a workspace each.
+ */
+#define MOE_DECODE_MAX_TOKENS 16
+moe_status moe_decode(const moe_layer_desc* desc, int T, const moe_bf16* x, const int32_t* token_ids,
+                      const int32_t* tid2eid, int vocab, const float* w_gate, const float* bias,
+                      const float* logit_offset, const moe_bf16* w1, const moe_bf16* w3,
+                      const moe_bf16* w2, moe_bf16* y, float* weights_out, int32_t* indices_out,
+                      int32_t* counts_out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Auxiliary-loss-free balancing step ("From One Giant FFN to 384 Tiny Experts", section 6, the bias
  * update run once per training step): with the balanced load T * topk / E, bias[e] -= gamma where
  * counts[e] is above it, bias[e] += gamma where below, unchanged where equal (compared exactly as
@@ -377,6 +398,18 @@ moe_status moe_forward_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* 
                              const moe_mxfp4_weights* weights_mxfp4, moe_bf16* y, float* weights_out,
                              int32_t* indices_out, int32_t* counts_out, void* ws, size_t ws_bytes,
                              moe_stream_t stream);
+
+/*
+ * moe_decode with MXFP4 expert weights (as for moe_expert_ffn_mxfp4: dim % 512 == 0, inter_dim % 512
+ * == 0).  The weights are used exactly and the activations in bf16 -- the values of
+ * MOE_OPT_MXFP4_BF16_ACTIVATIONS, whether the option is set or not.
+ */
+moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x,
+                            const int32_t* token_ids, const int32_t* tid2eid, int vocab,
+                            const float* w_gate, const float* bias, const float* logit_offset,
+                            const moe_mxfp4_weights* weights_mxfp4, moe_bf16* y, float* weights_out,
+                            int32_t* indices_out, int32_t* counts_out, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns the first error a kernel recorded in `ws` since the last

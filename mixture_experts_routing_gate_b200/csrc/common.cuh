@@ -25,7 +25,9 @@ struct ErrorWord {
   int status;           // 0 or the first moe_status recorded
   int info;             // the offending value (index, token id, or a wait site)
   int dispatch_ticket;  // dispatch's count of finished histogram blocks (0 between calls)
-  int pad[61];
+  int decode_arrive[3]; // the one-launch layer's grid barriers: CTAs arrived (0 between calls)
+  int decode_done;      //   and CTAs finished
+  int pad[57];
 };
 
 __device__ __forceinline__ void record_error(ErrorWord* ew, int status, int info) {

@@ -144,6 +144,37 @@ constexpr int kGemmSingle = 0;  // one 128-row weight tile per token chunk
 constexpr int kGemmSwiGLU = 1;  // w1 and w3 tiles of the same rows, SwiGLU epilogue
 constexpr int kGemmPair = 2;    // two adjacent 128-row weight tiles
 
+// The whole layer for a few tokens (decode.cu).
+constexpr int kDecodeMaxTokens = MOE_DECODE_MAX_TOKENS;
+struct DecodeParams {
+  int T, d, E, G, g, k, I;
+  int score_func, renorm;
+  float route_scale, swiglu_limit;
+  int weight_in_expert;       // routed rows of h carry their weights, the combine adds unweighted rows
+  int vocab;                  // > 0 with token_ids and tid2eid: the token-id table routes
+  int gate_splits;            // slices of k of the router logits
+  int ring_bytes;             // set by the launcher
+  int test_stall;             // failure-detection test hook: the producers issue no loads
+  const int32_t* token_ids;   // [T] or null
+  const int32_t* tid2eid;     // [vocab, k]
+  const float* w_gate;        // [E, d]
+  const float* bias;          // [E] or null
+  const float* logit_offset;  // [E] or null
+  const __nv_bfloat16* x;     // [T, d]
+  const uint8_t *w1, *w3, *w2;     // bf16 rows, or packed E2M1 codes
+  const uint8_t *w1s, *w3s, *w2s;  // UE8M0 block scales (MXFP4), else null
+  float* partial;             // [gate_splits, T, E] scratch
+  __nv_bfloat16* h;           // [T + T * k, I] scratch: shared rows first, then the active experts'
+  float* out;                 // [T + T * k, d] scratch
+  __nv_bfloat16* y;           // [T, d]
+  float* weights_out;         // [T, k] or null
+  int32_t* indices_out;       // [T, k] or null
+  int32_t* counts_out;        // [E] or null
+  ErrorWord* ew;
+};
+int decode_gate_splits(int E, int d);
+cudaError_t launch_layer_decode(DecodeParams p, bool fp4, int num_sms, cudaStream_t stream);
+
 // Host-side launchers, one per kernel; each returns the launch's cudaError_t.
 cudaError_t launch_gate_planes(const float* w, __nv_bfloat16* planes, long n, int* inexact_flag, int num_sms,
                                cudaStream_t stream);

@@ -81,7 +81,7 @@ namespace {
 // first, the scales 1 KiB-aligned after them) and the quantised x in a region of its own.
 struct WsLayout {
   size_t err, flag, planes, indices, weights, counts, offsets, row_of_slot, tok_of_row, w_perm, hist, base,
-      chunk_prefix, x_perm, h, out_perm, out_shared, xq, total;
+      chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, total;
   size_t xp_scales, h_scales, xq_scales;   // offsets of the scales inside x_perm, h and xq
 };
 
@@ -119,6 +119,10 @@ WsLayout ws_layout(const moe_layer_desc& d, int T) {
   L.out_shared = take((size_t)T * D * 2);
   L.xq = take(codes_and_scales((size_t)T * D));
   L.xq_scales = L.xq + align_up((size_t)T * D);
+  // the one-launch layer's partial logits and fp32 expert rows (batches it takes only)
+  const bool dec = T <= MOE_DECODE_MAX_TOKENS;
+  L.dec_partial = take(dec ? (size_t)moe::decode_gate_splits(d.n_experts, d.dim) * T * E * 4 : 0);
+  L.dec_out = take(dec ? (S + T) * D * 4 : 0);
   L.total = o;
   return L;
 }
@@ -816,6 +820,60 @@ moe_status forward_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, co
   return run_combine(d, T, out_perm, row_of_slot, w_perm ? nullptr : weights, out_shared, y, s);
 }
 
+// The whole layer in one launch (T <= MOE_DECODE_MAX_TOKENS).
+moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, const int32_t* token_ids,
+                       const int32_t* tid2eid, int vocab, const float* w_gate, const float* bias,
+                       const float* logit_offset, const moe_bf16* w1, const moe_bf16* w3, const moe_bf16* w2,
+                       const moe_mxfp4_weights* fp4, moe_bf16* y, float* weights_out, int32_t* indices_out,
+                       int32_t* counts_out, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const bool hashed = token_ids != nullptr || tid2eid != nullptr;
+  if (T < 0) return MOE_ERR_INVALID;
+  if (T > MOE_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (hashed && (token_ids == nullptr || tid2eid == nullptr || vocab <= 0)) return MOE_ERR_INVALID;
+  if (hashed && desc->score_func == MOE_SCORE_SOFTMAX) return MOE_ERR_UNSUPPORTED;
+  if (fp4 != nullptr) {
+    moe_layer_desc d4 = *desc;
+    d4.options |= MOE_OPT_MXFP4_BF16_ACTIVATIONS;   // this path's activations: 16-byte aligned codes suffice
+    MOE_TRY(check_mxfp4(d4, T, fp4));
+  }
+  if (T > 0 && (x == nullptr || w_gate == nullptr || y == nullptr)) return MOE_ERR_INVALID;
+  if (T > 0 && fp4 == nullptr && (w1 == nullptr || w3 == nullptr || w2 == nullptr)) return MOE_ERR_INVALID;
+  if (T > 0 && (!aligned16(x) || !aligned16(w_gate) || !aligned16(y))) return MOE_ERR_INVALID;
+  if (T > 0 && fp4 == nullptr && (!aligned16(w1) || !aligned16(w3) || !aligned16(w2))) return MOE_ERR_INVALID;
+  MOE_TRY(check_ws(*desc, T, ws, ws_bytes));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (counts_out != nullptr) return cuda_status(cudaMemsetAsync(counts_out, 0, sizeof(int32_t) * desc->n_experts, s));
+    return MOE_OK;
+  }
+  const moe_layer_desc& d = *desc;
+  const WsLayout L = ws_layout(d, T);
+  moe::DecodeParams p{};
+  p.T = T; p.d = d.dim; p.E = d.n_experts; p.G = d.n_groups; p.g = d.n_limited_groups; p.k = d.topk; p.I = d.inter_dim;
+  p.score_func = d.score_func; p.renorm = d.renorm; p.route_scale = d.route_scale; p.swiglu_limit = d.swiglu_limit;
+  p.weight_in_expert = d.weight_in_expert;
+  p.vocab = vocab; p.token_ids = token_ids; p.tid2eid = tid2eid;
+  p.gate_splits = moe::decode_gate_splits(d.n_experts, d.dim);
+  p.test_stall = test_stall_flag();
+  p.w_gate = w_gate; p.bias = hashed ? nullptr : bias; p.logit_offset = hashed ? nullptr : logit_offset;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
+  if (fp4 != nullptr) {
+    p.w1 = fp4->w1; p.w3 = fp4->w3; p.w2 = fp4->w2;
+    p.w1s = fp4->w1_scale; p.w3s = fp4->w3_scale; p.w2s = fp4->w2_scale;
+  } else {
+    p.w1 = bytes(w1); p.w3 = bytes(w3); p.w2 = bytes(w2);
+  }
+  p.partial = at<float>(ws, L.dec_partial);
+  p.h = at<__nv_bfloat16>(ws, L.h);
+  p.out = at<float>(ws, L.dec_out);
+  p.y = reinterpret_cast<__nv_bfloat16*>(y);
+  p.weights_out = weights_out; p.indices_out = indices_out; p.counts_out = counts_out;
+  p.ew = at<ErrorWord>(ws, L.err);
+  return cuda_status(moe::launch_layer_decode(p, fp4 != nullptr, num_sms(), s));
+}
+
 }  // namespace
 
 // =============================================================================================
@@ -1002,6 +1060,27 @@ moe_status moe_expert_ffn_mxfp4_gather(const moe_layer_desc* desc, int T, const 
   if (weights_mxfp4 == nullptr) return MOE_ERR_INVALID;
   return expert_ffn_entry(desc, T, nullptr, tok_of_row, offsets, row_weights, x, nullptr, nullptr, nullptr,
                           weights_mxfp4, out_perm, out_shared, ws, ws_bytes, stream);
+}
+
+moe_status moe_decode(const moe_layer_desc* desc, int T, const moe_bf16* x, const int32_t* token_ids,
+                      const int32_t* tid2eid, int vocab, const float* w_gate, const float* bias,
+                      const float* logit_offset, const moe_bf16* w1, const moe_bf16* w3, const moe_bf16* w2,
+                      moe_bf16* y, float* weights_out, int32_t* indices_out, int32_t* counts_out, void* ws,
+                      size_t ws_bytes, moe_stream_t stream) {
+  NvtxRange nvtx("moe_decode");
+  return decode_impl(desc, T, x, token_ids, tid2eid, vocab, w_gate, bias, logit_offset, w1, w3, w2, nullptr, y,
+                     weights_out, indices_out, counts_out, ws, ws_bytes, stream);
+}
+
+moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x, const int32_t* token_ids,
+                            const int32_t* tid2eid, int vocab, const float* w_gate, const float* bias,
+                            const float* logit_offset, const moe_mxfp4_weights* weights_mxfp4, moe_bf16* y,
+                            float* weights_out, int32_t* indices_out, int32_t* counts_out, void* ws, size_t ws_bytes,
+                            moe_stream_t stream) {
+  NvtxRange nvtx("moe_decode_mxfp4");
+  if (weights_mxfp4 == nullptr) return MOE_ERR_INVALID;
+  return decode_impl(desc, T, x, token_ids, tid2eid, vocab, w_gate, bias, logit_offset, nullptr, nullptr, nullptr,
+                     weights_mxfp4, y, weights_out, indices_out, counts_out, ws, ws_bytes, stream);
 }
 
 moe_status moe_get_error(void* ws, moe_stream_t stream, int32_t* info) {

@@ -345,3 +345,42 @@ def test_gate_prepare_rejects_bad_arguments(moe):
     assert lib.moe_gate(ctypes.byref(d), 4, fake, fake, None, None, fake, fake, fake, 1 << 30, None) == \
         moe.MOE_ERR_INVALID
     assert lib.moe_gate_prepared_bytes(ctypes.byref(d)) == 0
+
+
+def test_decode_rejects_bad_arguments_before_launch(moe):
+    cfg = W.CONFIGS["tiny"]
+    P = ctypes.c_void_p
+    fake, odd = P(1 << 20), P((1 << 20) + 8)   # never dereferenced: every call must fail its checks first
+
+    def call(desc=None, T=4, x=fake, ids=None, table=None, vocab=0, wg=fake, w1=fake, w3=fake, w2=fake, y=fake, ws=fake,
+             n=1 << 30):
+        d = desc or moe.layer_desc(cfg)
+        return moe.lib.moe_decode(ctypes.byref(d), T, x, ids, table, vocab, wg, None, None, w1, w3, w2, y, None, None,
+                                  None, ws, n, None)
+
+    assert call(T=-1) == moe.MOE_ERR_INVALID
+    assert call(T=moe.MOE_DECODE_MAX_TOKENS + 1) == moe.MOE_ERR_UNSUPPORTED
+    for name in ("x", "wg", "w1", "w3", "w2", "y"):
+        assert call(**{name: None}) == moe.MOE_ERR_INVALID, name
+        assert call(**{name: odd}) == moe.MOE_ERR_INVALID, name
+    assert call(ids=fake) == moe.MOE_ERR_INVALID
+    assert call(ids=fake, table=fake, vocab=0) == moe.MOE_ERR_INVALID
+    soft = moe.layer_desc(cfg.replace(score_func="softmax"))
+    assert call(desc=soft, ids=fake, table=fake, vocab=9) == moe.MOE_ERR_UNSUPPORTED
+    assert call(ws=None) == moe.MOE_ERR_WORKSPACE
+    assert call(ws=P((1 << 20) + 16)) == moe.MOE_ERR_WORKSPACE
+    assert call(n=moe.moe_workspace_bytes(moe.layer_desc(cfg), 4) - 1) == moe.MOE_ERR_WORKSPACE
+    bad = moe.layer_desc(cfg)
+    bad.topk = 9
+    assert call(desc=bad) != moe.MOE_OK
+    # MXFP4: the sizes and pointers of moe_expert_ffn_mxfp4
+    d = moe.layer_desc(cfg)   # dim 256: not a multiple of 512
+    w = moe.Mxfp4Weights(*[1 << 20] * 6)
+    args = lambda d, w: (ctypes.byref(d), 4, fake, None, None, 0, fake, None, None, w, fake, None, None, None, fake, 1 << 30, None)
+    assert moe.lib.moe_decode_mxfp4(*args(d, ctypes.byref(w))) == moe.MOE_ERR_UNSUPPORTED
+    d = moe.layer_desc(cfg.replace(dim=512, inter_dim=512))
+    assert moe.lib.moe_decode_mxfp4(*args(d, None)) == moe.MOE_ERR_INVALID
+    w.w2_scale = None
+    assert moe.lib.moe_decode_mxfp4(*args(d, ctypes.byref(w))) == moe.MOE_ERR_INVALID
+    w.w2_scale = (1 << 20) + 4
+    assert moe.lib.moe_decode_mxfp4(*args(d, ctypes.byref(w))) == moe.MOE_ERR_INVALID
