@@ -212,6 +212,16 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// The 3-D box at (c0 = innermost, c1, c2), as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Untiled bulk copies (cp.async.bulk): both addresses 16-byte aligned, the size a multiple of 16.
 // A load completes `bytes` of transaction count on `bar`; stores are tracked in the issuing thread's
 // bulk async-groups (bulk_commit closes a group, bulk_wait_read<N> waits until at most N of the most

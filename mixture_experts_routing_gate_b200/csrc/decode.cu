@@ -6,16 +6,19 @@
 // What bounds it: the weights of the chosen experts, read once -- every weight meets one to sixteen tokens,
 // far below the flops per byte at which the tensor cores would matter.  So the kernel is a weight stream:
 //
-// * one CTA per SM, all resident at once (cooperative launch), nine warps: a producer warp keeps bulk copies
-//   (cp.async.bulk, one contiguous piece of a weight row per lane) in flight into a byte ring of about
-//   190 KB of shared memory, eight consumer warps compute.  At 44 bytes/ns per SM the ring holds 4 us of
-//   the stream, more than the memory latency and more than a grid barrier, so the stream does not stop
-//   between the phases: the shared expert's first weights are loaded while the gate is computed, and the
-//   down projection's while the grid finishes the up projection (only the rows of h wait for the barrier).
+// * one CTA per SM, all resident at once (cooperative launch), nine warps: a producer warp keeps copies in
+//   flight into a byte ring of about 190 KB of shared memory, eight consumer warps compute.  At 44 bytes/ns
+//   per SM the ring holds 4 us of the stream, more than the memory latency and more than a grid barrier, so
+//   the stream does not stop between the phases: the shared expert's first weights are loaded while the gate
+//   is computed, and the down projection's while the grid finishes the up projection (only the rows of h
+//   wait for the barrier).  The weights come by TMA, 8 rows x 1 KB a copy: copies of single rows (1 KB) cost
+//   about 65 ns each whoever issues them and held the stream at 2 TB/s.  The token rows are gathered by
+//   cp.async of the producer's 32 lanes, which any row layout allows.
 // * the products run on mma.sync m16n8k16 with the weight rows as the 16-row operand and the tokens as the
 //   8 columns: at most two column tiles, so each weight is read from shared memory once.  The reduction
 //   index is permuted alike for both operands (thread t of a quad holds 8 consecutive elements), so that
-//   every fragment is one conflict-free 16-byte shared load (rows 64 bytes off a multiple of 128).
+//   every fragment is one conflict-free 16-byte shared load (weights: TMA's 128-byte swizzle; token rows
+//   64 bytes off a multiple of 128 apart).
 //   The eight warps split each stage along k and add their fp32 accumulators through shared memory in warp
 //   order: nothing depends on scheduling.
 // * an up-projection tile is 8 features: rows 0-7 of the MMA are w1's, rows 8-15 w3's, so gate and value of
@@ -52,7 +55,7 @@ constexpr int kRedPitch = 20;       // floats per token column of the warp-parti
 constexpr int kRedFloats = kConsumerWarps * kMaxT * kRedPitch;
 constexpr int kGateRows = 16;       // router rows per unit of the logit phase
 static_assert(2 * kRedFloats >= kConsumerWarps * 512, "the selection's scores share the exchange buffer");
-static_assert(kMaxT <= 16, "lanes 16-31 of the producer copy the token rows");
+static_assert(kMaxT <= 16, "two column tiles of eight tokens");
 
 struct DecodeSmem {
   uint64_t full[kSlots];
@@ -84,7 +87,13 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 __device__ __forceinline__ void red_release_add(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// 16 bytes global -> shared past L1, and this lane's arrival on a barrier once its copies so far landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // Waits until `*counter` reaches `target` (every CTA of the grid arrived).  Bounded as mbar_wait is.
 __device__ __forceinline__ bool grid_wait(const int* counter, int target, volatile int* abort, ErrorWord* ew, int site) {
@@ -124,16 +133,19 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // ------------------------------------------------------------------------------------------------
 // stage layout
 // ------------------------------------------------------------------------------------------------
-// A stage holds kChunk elements of k of 16 weight rows and of the tile's n token rows.
+// A stage holds kChunk elements of k of 16 weight rows and of the tile's n token rows.  The weights are two
+// blocks of 8 rows, each as TMA writes a box of 128 bytes x 8 rows x kBoxes in the 128-byte swizzle: the
+// 16-byte unit u of row r of box b lies at b * 1024 + r * 128 + ((u ^ r) << 4).
 template <bool kFp4>
 struct Stage {
   static constexpr int kChunk = kFp4 ? 1024 : 512;
-  static constexpr int kWPitch = kFp4 ? 512 + 16 : 1024 + 64;  // bytes; fp4: 8 rows x 16 bytes hit 32 banks
+  static constexpr int kBoxes = kFp4 ? 4 : 8;                  // of 256 codes or 64 bf16
+  static constexpr int kBlock = kBoxes * 1024;
   static constexpr int kSPitch = kFp4 ? 48 : 0;                // scale rows (32 bytes)
   static constexpr int kTPitch = kChunk * 2 + 64;
-  static constexpr int kSOff = 16 * kWPitch;
+  static constexpr int kSOff = 2 * kBlock;
   static constexpr int kTOff = kSOff + 16 * kSPitch;
-  __device__ static int bytes(int n) { return (kTOff + n * kTPitch + 127) & ~127; }
+  __device__ static int bytes(int n) { return (kTOff + n * kTPitch + 1023) & ~1023; }
 };
 
 // Where stage after stage lies in the ring: contiguous, back to the start when one does not fit.
@@ -492,31 +504,32 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int kw, int warp, 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t tok = stage + S::kTOff + g * S::kTPitch + t * 16;
   if (!kFp4) {
-    const uint32_t wr = stage + g * S::kWPitch + t * 16;
+    if (warp * 64 >= kw) return;   // the warp's 64 elements are box `warp`
+    const uint32_t wr = stage + warp * 1024 + g * 128;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const int ko = warp * 64 + kb * 32;
-      if (ko < kw) {
-        const uint4 lo = lds128(wr + ko * 2), hi = lds128(wr + 8 * S::kWPitch + ko * 2);
+      const uint32_t at = wr + (((kb * 4 + t) ^ g) << 4);
+      const uint4 lo = lds128(at), hi = lds128(at + S::kBlock);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 b = lds128(tok + nt * 8 * S::kTPitch + ko * 2);
-          mma_bf16(acc[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-          mma_bf16(acc[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 b = lds128(tok + nt * 8 * S::kTPitch + ko * 2);
+        mma_bf16(acc[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+        mma_bf16(acc[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
       }
     }
   } else {
-    const int k0 = warp * 128;
+    const int k0 = warp * 128;     // half of box warp / 2
     if (k0 >= kw) return;
-    const uint32_t wr = stage + g * S::kWPitch + t * 4, sr = stage + S::kSOff + g * S::kSPitch + warp * 4;
+    const uint32_t wr = stage + (warp >> 1) * 1024 + g * 128 + t * 4, sr = stage + S::kSOff + g * S::kSPitch + warp * 4;
     const uint32_t s_lo = checked_scales(lds32(sr), ew), s_hi = checked_scales(lds32(sr + 8 * S::kSPitch), ew);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       const int ko = k0 + kb * 32;
+      const uint32_t at = wr + ((((warp & 1) * 4 + kb) ^ g) << 4);
       uint32_t lo[4], hi[4];
-      e2m1_pairs(lds32(wr + ko / 2), lo);
-      e2m1_pairs(lds32(wr + 8 * S::kWPitch + ko / 2), hi);
+      e2m1_pairs(lds32(at), lo);
+      e2m1_pairs(lds32(at + S::kBlock), hi);
       const float f_lo = __uint_as_float(((s_lo >> (8 * kb)) & 0xFFu) << 23);
       const float f_hi = __uint_as_float(((s_hi >> (8 * kb)) & 0xFFu) << 23);
 #pragma unroll
@@ -564,6 +577,7 @@ template <bool kFp4>
 struct Producer {
   using S = Stage<kFp4>;
   const DecodeParams& p;
+  const CUtensorMap *map_w1, *map_w3, *map_w2;
   DecodeSmem* sm;
   uint8_t* ring;
   int lane;
@@ -571,7 +585,9 @@ struct Producer {
   int used = 0, outstanding = 0, npend = 0;
   bool h_ready = false;
 
-  __device__ Producer(const DecodeParams& p_, DecodeSmem* sm_, uint8_t* ring_, int lane_) : p(p_), sm(sm_), ring(ring_), lane(lane_) {}
+  __device__ Producer(const DecodeParams& p_, const CUtensorMap* w1, const CUtensorMap* w3, const CUtensorMap* w2,
+                      DecodeSmem* sm_, uint8_t* ring_, int lane_)
+      : p(p_), map_w1(w1), map_w3(w3), map_w2(w2), sm(sm_), ring(ring_), lane(lane_) {}
 
   // Room for a stage: its offset in the ring, or -1 after an abort.
   __device__ int acquire(int bytes) {
@@ -592,14 +608,19 @@ struct Producer {
     return off;
   }
 
+  // The stage's token rows, 16 bytes a lane and copy, and the lanes' arrivals for them.
   __device__ void copy_tokens(bool down, int a, int k0, int kw, int off, int slot) {
     const int n = sm->act_n[a], r0 = sm->act_off[a];
-    for (int i = kFp4 ? lane : lane - 16; i < n; i += 32) {
-      if (i < 0) continue;
-      const __nv_bfloat16* src = down ? p.h + (size_t)(r0 + i) * p.I + k0
-                                      : p.x + (size_t)(a == 0 ? i : sm->tok_of_row[r0 + i]) * p.d + k0;
-      bulk_load(ring + off + S::kTOff + i * S::kTPitch, src, kw * 2, &sm->full[slot]);
+    const uint32_t dst = smem_u32(ring + off + S::kTOff);
+    for (int i = 0; i < n; ++i) {
+      const __nv_bfloat16* src = down ? p.h + (size_t)(r0 + i) * p.I + k0 : p.x + (size_t)sm->tok_of_row[r0 + i] * p.d + k0;
+#pragma unroll
+      for (int u = 0; u < S::kChunk / 256; ++u) {
+        const int at = (u * 32 + lane) * 8;
+        if (at < kw) cp_async16(dst + i * S::kTPitch + at * 2, src + at);
+      }
     }
+    cp_async_arrive(&sm->full[slot]);
   }
 
   // The rows of h of the pending stages, once the whole grid has written h.
@@ -608,7 +629,7 @@ struct Producer {
     if (!h_ready) {
       if (lane == 0) ok = grid_wait(&p.ew->decode_arrive[1], (int)gridDim.x, &sm->abort, p.ew, 402);
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      fence_proxy_async_all();
+      __syncwarp();
       h_ready = true;   // after an abort too: the copies below stay in bounds and let the stages complete
     }
     for (int i = 0; i < npend; ++i) {
@@ -622,25 +643,25 @@ struct Producer {
   // All stages of a tile: block blk of 16 weight rows (8 + 8 in the up projections) of active expert a.
   __device__ bool tile(bool down, int a, int blk) {
     const int K = down ? p.I : p.d, n = sm->act_n[a], e = sm->act_e[a];
-    const int r = lane & 15;
-    const size_t row = down ? (size_t)e * p.d + blk * 16 + r : (size_t)e * p.I + blk * 8 + (r & 7);
-    const uint8_t* w = down ? p.w2 : (r < 8 ? p.w1 : p.w3);
-    const uint8_t* ws = down ? p.w2s : (r < 8 ? p.w1s : p.w3s);
+    const int row = down ? e * p.d + blk * 16 : e * p.I + blk * 8;
+    const int box = kFp4 ? 256 : 64;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
       const int kw = min(S::kChunk, K - k0);
       const int off = acquire(S::bytes(n));
       if (off < 0) return false;
       uint64_t* bar = &sm->full[pos.slot];
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar, (kFp4 ? 16 * (kw / 2 + kw / 32) : 16 * kw * 2) + n * kw * 2);
-      __syncwarp();
-      if (lane < 16) {
-        if (kFp4)
-          bulk_load(ring + off + r * S::kWPitch, w + (row * K + k0) / 2, kw / 2, bar);
-        else
-          bulk_load(ring + off + r * S::kWPitch, w + (row * K + k0) * 2, kw * 2, bar);
-      } else if (kFp4) {
-        bulk_load(ring + off + S::kSOff + r * S::kSPitch, ws + (row * K + k0) / 32, kw / 32, bar);
+      if (lane == 0) {
+        uint8_t* dst = ring + off;
+        mbar_arrive_expect_tx(bar, 2 * S::kBlock);   // whole boxes: what lies past K is filled with zeros
+        tma_load_3d(dst, down ? map_w2 : map_w1, bar, 0, row, k0 / box);
+        tma_load_3d(dst + S::kBlock, down ? map_w2 : map_w3, bar, 0, down ? row + 8 : row, k0 / box);
+      }
+      if (kFp4) {   // scales: 32 bytes of each of the 16 rows
+        const int r = lane >> 1, half = lane & 1;
+        const uint8_t* ws = down ? p.w2s : (r < 8 ? p.w1s : p.w3s);
+        if (half * 512 < kw)
+          cp_async16(smem_u32(ring + off + S::kSOff + r * S::kSPitch + half * 16),
+                     ws + ((size_t)(row + (down ? r : r & 7)) * K + k0) / 32 + half * 16);
       }
       if (!down || h_ready) {
         copy_tokens(down, a, k0, kw, off, pos.slot);
@@ -676,15 +697,17 @@ struct Producer {
 };
 
 template <bool kFp4>
-__global__ void __launch_bounds__(kDecThreads, 1) layer_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, 1)
+    layer_decode_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w3,
+                        const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ DecodeParams p) {
   using S = Stage<kFp4>;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DecodeSmem* sm = reinterpret_cast<DecodeSmem*>(ring + p.ring_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sm->full[i], 1);
+      mbar_init(&sm->full[i], 1 + 32);   // the weights' arrival and the lanes' token copies
       mbar_init(&sm->empty[i], kConsumerWarps);
     }
     mbar_init(&sm->routed, 1);
@@ -693,12 +716,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) layer_decode_kernel(const __gr
     sm->act_e[0] = p.E;
     sm->act_off[0] = 0;
     sm->act_n[0] = p.T;
+    for (int i = 0; i < p.T; ++i) sm->tok_of_row[i] = i;
     fence_barrier_init();
+    tma_prefetch_desc(&map_w1);
+    tma_prefetch_desc(&map_w3);
+    tma_prefetch_desc(&map_w2);
   }
   __syncthreads();
 
   if (warp == kConsumerWarps) {
-    Producer<kFp4> pr(p, sm, ring, lane);
+    Producer<kFp4> pr(p, &map_w1, &map_w3, &map_w2, sm, ring, lane);
     pr.run();
   } else {
     volatile int* abort = &sm->abort;
@@ -775,7 +802,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) layer_decode_kernel(const __gr
     const int nb1 = p.I / 8, nb2 = p.d / 16, na = sm->n_act;
     for (int j = blockIdx.x; j < na * nb1; j += G) run_tile(std::false_type{}, j / nb1, j % nb1);
     __threadfence();
-    fence_proxy_async_all();   // h is read by bulk copies
     consumer_sync();
     if (tid == 0) red_release_add(&p.ew->decode_arrive[1], 1);
     for (int j = blockIdx.x; j < na * nb2; j += G) run_tile(std::true_type{}, j / nb2, j % nb2);
@@ -830,9 +856,10 @@ int decode_gate_splits(int E, int d) {
   return std::max(1, std::min(d / 128, 148 / (E / kGateRows)));
 }
 
-cudaError_t launch_layer_decode(DecodeParams p, bool fp4, int num_sms, cudaStream_t stream) {
+cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
+                                bool fp4, int num_sms, cudaStream_t stream) {
   const size_t smem = 227 * 1024;
-  p.ring_bytes = (int)((smem - 128 - sizeof(DecodeSmem)) / 128 * 128);
+  p.ring_bytes = (int)((smem - 1024 - sizeof(DecodeSmem)) / 1024 * 1024);
   auto kernel = fp4 ? layer_decode_kernel<true> : layer_decode_kernel<false>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -849,7 +876,7 @@ cudaError_t launch_layer_decode(DecodeParams p, bool fp4, int num_sms, cudaStrea
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, w1, w3, w2, p);
 }
 
 }  // namespace moe

@@ -173,7 +173,10 @@ struct DecodeParams {
   ErrorWord* ew;
 };
 int decode_gate_splits(int E, int d);
-cudaError_t launch_layer_decode(DecodeParams p, bool fp4, int num_sms, cudaStream_t stream);
+// w1 / w3 / w2: the stacked expert matrices as [128 bytes, rows, bytes of a row / 128] in boxes of
+// 128 bytes x 8 rows x 8 (bf16) or 4 (packed codes), 128-byte swizzle.
+cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
+                                bool fp4, int num_sms, cudaStream_t stream);
 
 // Host-side launchers, one per kernel; each returns the launch's cudaError_t.
 cudaError_t launch_gate_planes(const float* w, __nv_bfloat16* planes, long n, int* inexact_flag, int num_sms,

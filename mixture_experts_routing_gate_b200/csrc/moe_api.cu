@@ -233,6 +233,22 @@ bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of row_bytes bytes (a multiple of 128) cut into 128-byte columns: [128 bytes, rows, row_bytes / 128],
+// boxes of 128 bytes x box_rows x box_cols in the 128-byte swizzle -- one copy brings box_cols * 128
+// contiguous bytes of each of box_rows rows.
+bool make_map_columns(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                      uint32_t box_cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {128, rows, row_bytes / 128};
+  const cuuint64_t strides[2] = {row_bytes, 128};
+  const cuuint32_t box[3] = {128, box_rows, box_cols};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)                      \
@@ -871,7 +887,14 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.weights_out = weights_out; p.indices_out = indices_out; p.counts_out = counts_out;
   p.ew = at<ErrorWord>(ws, L.err);
-  return cuda_status(moe::launch_layer_decode(p, fp4 != nullptr, num_sms(), s));
+  CUtensorMap m1, m3, m2;
+  const uint64_t n = d.n_experts + 1, per = fp4 != nullptr ? 1 : 4;   // bytes of two weights
+  const uint32_t cols = fp4 != nullptr ? 4 : 8;
+  if (!make_map_columns(&m1, p.w1, n * d.inter_dim, d.dim / 2 * per, 8, cols) ||
+      !make_map_columns(&m3, p.w3, n * d.inter_dim, d.dim / 2 * per, 8, cols) ||
+      !make_map_columns(&m2, p.w2, n * d.dim, d.inter_dim / 2 * per, 8, cols))
+    return MOE_ERR_CUDA;
+  return cuda_status(moe::launch_layer_decode(m1, m3, m2, p, fp4 != nullptr, num_sms(), s));
 }
 
 }  // namespace
