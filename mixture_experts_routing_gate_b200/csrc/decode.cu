@@ -6,21 +6,19 @@
 // What bounds it: the weights of the chosen experts, read once -- every weight meets one to sixteen tokens,
 // far below the flops per byte at which the tensor cores would matter.  So the kernel is a weight stream:
 //
-// * one CTA per SM, all resident at once (cooperative launch), nine warps: a producer warp keeps copies in
-//   flight into a byte ring of about 190 KB of shared memory, eight consumer warps compute.  At 44 bytes/ns
-//   per SM the ring holds 4 us of the stream, more than the memory latency and more than a grid barrier, so
-//   the stream does not stop between the phases: the shared expert's first weights are loaded while the gate
-//   is computed, and the down projection's while the grid finishes the up projection (only the rows of h
-//   wait for the barrier).  The weights come by TMA, 8 rows x 1 KB a copy: copies of single rows (1 KB) cost
-//   about 65 ns each whoever issues them and held the stream at 2 TB/s.  The token rows are gathered by
-//   cp.async of the producer's 32 lanes, which any row layout allows.
+// * one CTA per SM, all resident at once (cooperative launch), 17 warps: one producer thread keeps TMA copies
+//   of 8 rows x 1 KB in flight into a ring of about 180 KB of shared memory, sixteen consumer warps compute.
+//   At 44 bytes/ns per SM the ring holds 4 us of the stream, more than the memory latency and more than a
+//   grid barrier, so the stream does not stop between the phases: the shared expert's first weights are
+//   loaded while the gate is computed, and the down projection's while the grid finishes the up projection.
+//   Copies of single rows (1 KB) cost about 65 ns each whoever issues them and held the stream at 2 TB/s.
 // * the products run on mma.sync m16n8k16 with the weight rows as the 16-row operand and the tokens as the
 //   8 columns: at most two column tiles, so each weight is read from shared memory once.  The reduction
 //   index is permuted alike for both operands (thread t of a quad holds 8 consecutive elements), so that
-//   every fragment is one conflict-free 16-byte shared load (weights: TMA's 128-byte swizzle; token rows
-//   64 bytes off a multiple of 128 apart).
-//   The eight warps split each stage along k and add their fp32 accumulators through shared memory in warp
-//   order: nothing depends on scheduling.
+//   a weight fragment is one conflict-free 16-byte shared load from TMA's 128-byte swizzle and a token
+//   fragment one 16-byte load from global memory (L1 or L2; loaded a stage ahead), whatever the token's row.
+//   Eight warps split a stage along k, the two groups of eight take alternate stages; the fp32 accumulators
+//   of a tile are added through shared memory in warp order: nothing depends on scheduling.
 // * an up-projection tile is 8 features: rows 0-7 of the MMA are w1's, rows 8-15 w3's, so gate and value of
 //   a feature meet in one accumulator tile.  A down-projection tile is 16 output features of one expert.
 // * four phases between three grid barriers: partial router logits (K split over the CTAs), then every CTA
@@ -44,10 +42,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kConsumerWarps = 8;
+constexpr int kConsumerWarps = 16;   // two groups of eight taking alternate stages
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kDecThreads = kConsumers + 32;
-constexpr int kSlots = 24;          // ring stages in flight, at most
+constexpr int kMaxStages = 24;
 constexpr int kMaxT = kDecodeMaxTokens;
 constexpr int kMaxS = kMaxT * kMaxRouteTopk;
 constexpr int kMaxAct = kMaxS + 1;  // active experts: the shared one and at most one per slot
@@ -58,8 +56,8 @@ static_assert(2 * kRedFloats >= kConsumerWarps * 512, "the selection's scores sh
 static_assert(kMaxT <= 16, "two column tiles of eight tokens");
 
 struct DecodeSmem {
-  uint64_t full[kSlots];
-  uint64_t empty[kSlots];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t routed;                  // the lists below are complete
   int abort;
   int n_act;                        // active experts, the shared one first
@@ -71,13 +69,15 @@ struct DecodeSmem {
   int tok_of_row[kMaxS + kMaxT];
   float row_w[kMaxS + kMaxT];
   int act_e[kMaxAct], act_off[kMaxAct], act_n[kMaxAct];
-  int charge[kSlots];               // ring bytes held by each stage (producer only)
-  int4 pend[kSlots];                // stages whose rows of h are still to be copied (producer only)
   alignas(16) float red[2][kRedFloats];
 };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-static_assert(kConsumers == 256, "the named barrier's thread count");
+// The consumer warps' barrier.  It takes whole warps, so lanes that waited on their own rejoin first.
+__device__ __forceinline__ void consumer_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 512;" ::: "memory");
+}
+static_assert(kConsumers == 512, "the named barrier's thread count");
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
   int v;
@@ -133,39 +133,38 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // ------------------------------------------------------------------------------------------------
 // stage layout
 // ------------------------------------------------------------------------------------------------
-// A stage holds kChunk elements of k of 16 weight rows and of the tile's n token rows.  The weights are two
-// blocks of 8 rows, each as TMA writes a box of 128 bytes x 8 rows x kBoxes in the 128-byte swizzle: the
-// 16-byte unit u of row r of box b lies at b * 1024 + r * 128 + ((u ^ r) << 4).
+// A stage holds kChunk elements of k of 16 weight rows: two blocks of 8 rows, each as TMA writes a box of
+// 128 bytes x 8 rows x kBoxes in the 128-byte swizzle -- the 16-byte unit u of row r of box b lies at
+// b * 1024 + r * 128 + ((u ^ r) << 4) -- and, for MXFP4, the rows' scales.
 template <bool kFp4>
 struct Stage {
   static constexpr int kChunk = kFp4 ? 1024 : 512;
   static constexpr int kBoxes = kFp4 ? 4 : 8;                  // of 256 codes or 64 bf16
   static constexpr int kBlock = kBoxes * 1024;
   static constexpr int kSPitch = kFp4 ? 48 : 0;                // scale rows (32 bytes)
-  static constexpr int kTPitch = kChunk * 2 + 64;
   static constexpr int kSOff = 2 * kBlock;
-  static constexpr int kTOff = kSOff + 16 * kSPitch;
-  __device__ static int bytes(int n) { return (kTOff + n * kTPitch + 1023) & ~1023; }
+  static constexpr int kBytes = (kSOff + 16 * kSPitch + 1023) & ~1023;
 };
 
-// Where stage after stage lies in the ring: contiguous, back to the start when one does not fit.
 struct RingPos {
-  int head = 0, slot = 0;
+  int slot = 0;
   uint32_t phase = 0;
-  __device__ int place(int bytes, int cap, int* charge) {
-    int off = head, c = bytes;
-    if (off + bytes > cap) {
-      c += cap - off;
-      off = 0;
-    }
-    head = off + bytes;
-    if (charge != nullptr) *charge = c;
-    return off;
+  __device__ void step(int by, int stages) {
+    for (slot += by; slot >= stages; slot -= stages) phase ^= 1;
   }
+};
+
+// Tile j of a phase as (active expert, block of rows), stepped by the grid without a division.
+struct TileIter {
+  int j, a, blk, step_a, step_b, nb;
+  __device__ TileIter(int nb_) : j(blockIdx.x), a(j / nb_), blk(j % nb_), step_a(gridDim.x / nb_), step_b(gridDim.x % nb_), nb(nb_) {}
   __device__ void next() {
-    if (++slot == kSlots) {
-      slot = 0;
-      phase ^= 1;
+    j += gridDim.x;
+    a += step_a;
+    blk += step_b;
+    if (blk >= nb) {
+      blk -= nb;
+      ++a;
     }
   }
 };
@@ -202,29 +201,31 @@ __device__ __forceinline__ int reduce_transposed(float (&v)[N], int lane) {
   return first;
 }
 
-// Unit u: 16 router rows x one slice of k.  Four warps take 4 rows each, twice over the slice's halves.
+// Unit u: 16 router rows x one slice of k.  Four warps take 4 rows each, on each quarter of the slice.
+// Tokens t0 to t0 + TT - 1.
 template <int TT>
-__device__ __forceinline__ void gate_partials(const DecodeParams& p, float* red, int warp, int lane) {
+__device__ __forceinline__ void gate_partials(const DecodeParams& p, int t0, float* red, int warp, int lane) {
   const int groups = p.E / kGateRows, units = groups * p.gate_splits;
   const int nb = p.d / 128;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int grp = u % groups, sp = u / groups;
-    const int b0 = sp * nb / p.gate_splits, b1 = (sp + 1) * nb / p.gate_splits, bm = (b0 + b1) >> 1;
     const int rsub = warp & 3, ksub = warp >> 2;
+    const int q0 = sp * nb / p.gate_splits, q1 = (sp + 1) * nb / p.gate_splits;
+    const int b0 = q0 + ((q1 - q0) * ksub >> 2), b1 = q0 + ((q1 - q0) * (ksub + 1) >> 2);
     const int e0 = grp * kGateRows + rsub * 4;
     float acc[4 * TT];
 #pragma unroll
     for (int i = 0; i < 4 * TT; ++i) acc[i] = 0.f;
 #pragma unroll 2
-    for (int b = ksub ? bm : b0; b < (ksub ? b1 : bm); ++b) {
+    for (int b = b0; b < b1; ++b) {
       const int k = b * 128 + lane * 4;
       float4 w[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) w[r] = __ldg(reinterpret_cast<const float4*>(p.w_gate + (size_t)(e0 + r) * p.d + k));
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        if (t < p.T) {
-          const uint2 xv = __ldg(reinterpret_cast<const uint2*>(p.x + (size_t)t * p.d + k));
+        if (t0 + t < p.T) {
+          const uint2 xv = __ldg(reinterpret_cast<const uint2*>(p.x + (size_t)(t0 + t) * p.d + k));
           const float x0 = __uint_as_float(xv.x << 16), x1 = __uint_as_float(xv.x & 0xffff0000u);
           const float x2 = __uint_as_float(xv.y << 16), x3 = __uint_as_float(xv.y & 0xffff0000u);
 #pragma unroll
@@ -246,9 +247,10 @@ __device__ __forceinline__ void gate_partials(const DecodeParams& p, float* red,
     const int tid = warp * 32 + lane;
     if (tid < kGateRows * TT) {
       const int t = tid / kGateRows, row = tid % kGateRows;
-      if (t < p.T) {
+      if (t0 + t < p.T) {
         const int at = (row >> 2) * 64 + t * 4 + (row & 3);
-        p.partial[((size_t)sp * p.T + t) * p.E + grp * kGateRows + row] = red[at] + red[at + 4 * 64];
+        p.partial[((size_t)sp * p.T + t0 + t) * p.E + grp * kGateRows + row] =
+            (red[at] + red[at + 4 * 64]) + (red[at + 8 * 64] + red[at + 12 * 64]);
       }
     }
     consumer_sync();
@@ -270,21 +272,23 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return max((b & 0x80000000u) ? ~b : b | 0x80000000u, 1u);
 }
 
+template <int PL>   // experts per lane: e = lane + 32 i
 __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem* sm, float* scores, int t, int lane) {
-  constexpr int PL = 16;   // experts per lane: e = lane + 32 i
   float sc[PL];
   uint32_t key[PL];
 #pragma unroll
+  for (int i = 0; i < PL; ++i) sc[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.gate_splits; ++s) {
+    const float* src = p.partial + ((size_t)s * p.T + t) * p.E;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) sc[i] += __ldcg(src + min(lane + 32 * i, p.E - 1));
+  }
+#pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 32 * i;
-    float v = -INFINITY;
-    if (e < p.E) {
-      v = 0.f;
-      const float* src = p.partial + (size_t)t * p.E + e;
-      for (int s = 0; s < p.gate_splits; ++s) v += __ldcg(src + (size_t)s * p.T * p.E);
-      if (p.logit_offset != nullptr) v += p.logit_offset[e];
-    }
-    sc[i] = v;
+    if (p.logit_offset != nullptr) sc[i] += __ldg(p.logit_offset + min(e, p.E - 1));
+    if (e >= p.E) sc[i] = -INFINITY;
   }
   if (p.score_func == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY, z = 0.f;
@@ -497,36 +501,55 @@ __device__ __forceinline__ uint32_t checked_scales(uint32_t s4, ErrorWord* ew) {
   return s4;
 }
 
+// The warp's token fragments of one stage: 16 bytes of each of its kBlocks blocks of 32 elements, for
+// token columns g and g + 8.
+template <bool kFp4, int kNT>
+struct TokenFrags {
+  static constexpr int kBlocks = kFp4 ? 4 : 2;
+  uint4 v[kNT][kBlocks];
+  // row: the columns' rows or null; k: first element of the warp's part, K: elements of a row
+  template <bool kDown>
+  __device__ __forceinline__ void load(const __nv_bfloat16* const (&row)[kNT], int k, int K, int t) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int kb = 0; kb < kBlocks; ++kb) {
+        v[nt][kb] = make_uint4(0u, 0u, 0u, 0u);
+        if (k < K && row[nt] != nullptr) {
+          const uint4* at = reinterpret_cast<const uint4*>(row[nt] + k + kb * 32 + t * 8);
+          v[nt][kb] = kDown ? __ldcg(at) : __ldg(at);   // h is written during this kernel: read from L2
+        }
+      }
+  }
+};
+
 // kPaired: the token rows already hold each octet in the order 0 4 1 5 2 6 3 7 (MXFP4's h).
-template <bool kFp4, bool kPaired, int NT>
-__device__ __forceinline__ void consume_stage(uint32_t stage, int kw, int warp, int lane, float (&acc)[2][4], ErrorWord* ew) {
+// w: the warp's place in its group of eight.
+template <bool kFp4, bool kPaired, int NT, int kNT>
+__device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT>& tok,
+                                              float (&acc)[kNT][4], ErrorWord* ew) {
   using S = Stage<kFp4>;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t tok = stage + S::kTOff + g * S::kTPitch + t * 16;
   if (!kFp4) {
-    if (warp * 64 >= kw) return;   // the warp's 64 elements are box `warp`
-    const uint32_t wr = stage + warp * 1024 + g * 128;
+    const uint32_t wr = stage + w * 1024 + g * 128;   // the warp's 64 elements are box w
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      const int ko = warp * 64 + kb * 32;
       const uint32_t at = wr + (((kb * 4 + t) ^ g) << 4);
       const uint4 lo = lds128(at), hi = lds128(at + S::kBlock);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint4 b = lds128(tok + nt * 8 * S::kTPitch + ko * 2);
+        const uint4 b = tok.v[nt][kb];
         mma_bf16(acc[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
         mma_bf16(acc[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
       }
     }
   } else {
-    const int k0 = warp * 128;     // half of box warp / 2
-    if (k0 >= kw) return;
-    const uint32_t wr = stage + (warp >> 1) * 1024 + g * 128 + t * 4, sr = stage + S::kSOff + g * S::kSPitch + warp * 4;
+    // the warp's 128 elements are half of box w / 2
+    const uint32_t wr = stage + (w >> 1) * 1024 + g * 128 + t * 4, sr = stage + S::kSOff + g * S::kSPitch + w * 4;
     const uint32_t s_lo = checked_scales(lds32(sr), ew), s_hi = checked_scales(lds32(sr + 8 * S::kSPitch), ew);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
-      const int ko = k0 + kb * 32;
-      const uint32_t at = wr + ((((warp & 1) * 4 + kb) ^ g) << 4);
+      const uint32_t at = wr + ((((w & 1) * 4 + kb) ^ g) << 4);
       uint32_t lo[4], hi[4];
       e2m1_pairs(lds32(at), lo);
       e2m1_pairs(lds32(at + S::kBlock), hi);
@@ -534,7 +557,7 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int kw, int warp, 
       const float f_hi = __uint_as_float(((s_hi >> (8 * kb)) & 0xFFu) << 23);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        uint4 b = lds128(tok + nt * 8 * S::kTPitch + ko * 2);
+        uint4 b = tok.v[nt][kb];
         if (!kPaired)
           b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
                          __byte_perm(b.y, b.w, 0x7632));
@@ -551,10 +574,11 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int kw, int warp, 
 }
 
 // The warp's accumulators of a tile into the exchange buffer, [warp][token column][kRedPitch rows].
-__device__ __forceinline__ void put_partials(float* red, int warp, int lane, const float (&acc)[2][4], int nt_used) {
+template <int kNT>
+__device__ __forceinline__ void put_partials(float* red, int warp, int lane, const float (&acc)[kNT][4], int nt_used) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
+  for (int nt = 0; nt < kNT; ++nt) {
     if (nt >= nt_used) break;
     float* c = red + (warp * kMaxT + nt * 8 + 2 * t) * kRedPitch + g;
     c[0] = acc[nt][0];
@@ -573,150 +597,82 @@ __device__ __forceinline__ float sum_partials(const float* red, int col, int row
 // ------------------------------------------------------------------------------------------------
 // the kernel
 // ------------------------------------------------------------------------------------------------
+// The weight stream: TMA copies by lane 0 and, for MXFP4, the scales by cp.async of all 32 lanes (then the
+// full barriers count their 32 arrivals too).
 template <bool kFp4>
-struct Producer {
+__device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap* map_w1, const CUtensorMap* map_w3,
+                                        const CUtensorMap* map_w2, DecodeSmem* sm, uint8_t* ring, int lane) {
   using S = Stage<kFp4>;
-  const DecodeParams& p;
-  const CUtensorMap *map_w1, *map_w3, *map_w2;
-  DecodeSmem* sm;
-  uint8_t* ring;
-  int lane;
-  RingPos pos, old;
-  int used = 0, outstanding = 0, npend = 0;
-  bool h_ready = false;
-
-  __device__ Producer(const DecodeParams& p_, const CUtensorMap* w1, const CUtensorMap* w3, const CUtensorMap* w2,
-                      DecodeSmem* sm_, uint8_t* ring_, int lane_)
-      : p(p_), map_w1(w1), map_w3(w3), map_w2(w2), sm(sm_), ring(ring_), lane(lane_) {}
-
-  // Room for a stage: its offset in the ring, or -1 after an abort.
-  __device__ int acquire(int bytes) {
-    int charge;
-    const int off = pos.place(bytes, p.ring_bytes, &charge);
-    while (used + charge > p.ring_bytes || outstanding == kSlots) {
-      if (npend > 0 && outstanding == npend && !flush()) return -1;
-      if (!mbar_wait_warp(&sm->empty[old.slot], old.phase, &sm->abort, p.ew, 401)) return -1;
-      used -= sm->charge[old.slot];
-      old.next();
-      --outstanding;
-    }
-    __syncwarp();
-    if (lane == 0) sm->charge[pos.slot] = charge;
-    __syncwarp();
-    used += charge;
-    ++outstanding;
-    return off;
-  }
-
-  // The stage's token rows, 16 bytes a lane and copy, and the lanes' arrivals for them.
-  __device__ void copy_tokens(bool down, int a, int k0, int kw, int off, int slot) {
-    const int n = sm->act_n[a], r0 = sm->act_off[a];
-    const uint32_t dst = smem_u32(ring + off + S::kTOff);
-    for (int i = 0; i < n; ++i) {
-      const __nv_bfloat16* src = down ? p.h + (size_t)(r0 + i) * p.I + k0 : p.x + (size_t)sm->tok_of_row[r0 + i] * p.d + k0;
-#pragma unroll
-      for (int u = 0; u < S::kChunk / 256; ++u) {
-        const int at = (u * 32 + lane) * 8;
-        if (at < kw) cp_async16(dst + i * S::kTPitch + at * 2, src + at);
-      }
-    }
-    cp_async_arrive(&sm->full[slot]);
-  }
-
-  // The rows of h of the pending stages, once the whole grid has written h.
-  __device__ bool flush() {
-    int ok = 1;
-    if (!h_ready) {
-      if (lane == 0) ok = grid_wait(&p.ew->decode_arrive[1], (int)gridDim.x, &sm->abort, p.ew, 402);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      __syncwarp();
-      h_ready = true;   // after an abort too: the copies below stay in bounds and let the stages complete
-    }
-    for (int i = 0; i < npend; ++i) {
-      const int4 q = sm->pend[i];
-      copy_tokens(true, q.x, q.y, min(S::kChunk, p.I - q.y), q.z, q.w);
-    }
-    npend = 0;
-    return ok != 0;
-  }
-
-  // All stages of a tile: block blk of 16 weight rows (8 + 8 in the up projections) of active expert a.
-  __device__ bool tile(bool down, int a, int blk) {
-    const int K = down ? p.I : p.d, n = sm->act_n[a], e = sm->act_e[a];
+  if (p.test_stall) return;
+  volatile int* abort = &sm->abort;
+  constexpr int kBox = kFp4 ? 256 : 64;
+  RingPos pos;
+  int issued = 0;
+  bool ok = true, routed = false;
+  auto tile = [&](bool down, int a, int blk) {
+    const int K = down ? p.I : p.d, e = sm->act_e[a];
     const int row = down ? e * p.d + blk * 16 : e * p.I + blk * 8;
-    const int box = kFp4 ? 256 : 64;
+    const CUtensorMap *m0 = down ? map_w2 : map_w1, *m1 = down ? map_w2 : map_w3;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
-      const int kw = min(S::kChunk, K - k0);
-      const int off = acquire(S::bytes(n));
-      if (off < 0) return false;
       uint64_t* bar = &sm->full[pos.slot];
-      if (lane == 0) {
-        uint8_t* dst = ring + off;
-        mbar_arrive_expect_tx(bar, 2 * S::kBlock);   // whole boxes: what lies past K is filled with zeros
-        tma_load_3d(dst, down ? map_w2 : map_w1, bar, 0, row, k0 / box);
-        tma_load_3d(dst + S::kBlock, down ? map_w2 : map_w3, bar, 0, down ? row + 8 : row, k0 / box);
-      }
-      if (kFp4) {   // scales: 32 bytes of each of the 16 rows
+      uint8_t* dst = ring + pos.slot * S::kBytes;
+      if (kFp4) {
+        if (!mbar_wait_warp(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
         const int r = lane >> 1, half = lane & 1;
         const uint8_t* ws = down ? p.w2s : (r < 8 ? p.w1s : p.w3s);
-        if (half * 512 < kw)
-          cp_async16(smem_u32(ring + off + S::kSOff + r * S::kSPitch + half * 16),
+        if (k0 + half * 512 < K)
+          cp_async16(smem_u32(dst + S::kSOff + r * S::kSPitch + half * 16),
                      ws + ((size_t)(row + (down ? r : r & 7)) * K + k0) / 32 + half * 16);
+        cp_async_arrive(bar);
+      } else if (lane == 0) {
+        if (!mbar_wait(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
       }
-      if (!down || h_ready) {
-        copy_tokens(down, a, k0, kw, off, pos.slot);
-      } else {
-        if (lane == 0) sm->pend[npend] = make_int4(a, k0, off, pos.slot);
-        __syncwarp();
-        ++npend;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, 2 * S::kBlock);   // whole boxes: what lies past K is filled with zeros
+        tma_load_3d(dst, m0, bar, 0, row, k0 / kBox);
+        tma_load_3d(dst + S::kBlock, m1, bar, 0, down ? row + 8 : row, k0 / kBox);
       }
-      pos.next();
+      ++issued;
+      pos.step(1, p.stages);
     }
     return true;
-  }
-
-  __device__ void run() {
-    if (p.test_stall) return;
-    bool ok = true, routed = false;
-    const int nb1 = p.I / 8, nb2 = p.d / 16;
-    for (int j = blockIdx.x; ok; j += gridDim.x) {
-      if (j >= nb1 && !routed) {
-        ok = mbar_wait_warp(&sm->routed, 0, &sm->abort, p.ew, 403);
-        routed = true;
-        if (!ok) break;
-      }
-      if (routed && j >= sm->n_act * nb1) break;
-      ok = tile(false, j / nb1, j % nb1);
+  };
+  const int nb1 = p.I / 8, nb2 = p.d / 16;
+  for (TileIter it(nb1); ok; it.next()) {
+    if (it.a > 0 && !routed) {
+      ok = kFp4 ? mbar_wait_warp(&sm->routed, 0, abort, p.ew, 403) : mbar_wait(&sm->routed, 0, abort, p.ew, 403);
+      routed = true;
+      if (!ok) break;
     }
-    for (int j = blockIdx.x; ok && j < sm->n_act * nb2; j += gridDim.x) ok = tile(true, j / nb2, j % nb2);
-    if (npend > 0) ok = flush() && ok;
-    if (!ok)   // let every copy already issued land before the CTA leaves
-      for (; outstanding > 0; --outstanding, old.next())
-        mbar_wait_warp(&sm->full[old.slot], old.phase, nullptr, nullptr, 0);
+    if (routed && it.a >= sm->n_act) break;
+    ok = tile(false, it.a, it.blk);
   }
-};
+  if (ok)
+    for (TileIter it(nb2); ok && it.a < sm->n_act; it.next()) ok = tile(true, it.a, it.blk);
+  if (!ok) {   // let every copy already issued land before the CTA leaves
+    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+      mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+  }
+}
 
-template <bool kFp4>
+// kNT: column tiles of eight tokens (1 for batches of at most 8, whose fragments then take half the registers).
+template <bool kFp4, int kNT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     layer_decode_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w3,
                         const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ DecodeParams p) {
   using S = Stage<kFp4>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  DecodeSmem* sm = reinterpret_cast<DecodeSmem*>(ring + p.ring_bytes);
+  DecodeSmem* sm = reinterpret_cast<DecodeSmem*>(ring + p.stages * S::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sm->full[i], 1 + 32);   // the weights' arrival and the lanes' token copies
-      mbar_init(&sm->empty[i], kConsumerWarps);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&sm->full[i], kFp4 ? 1 + 32 : 1);
+      mbar_init(&sm->empty[i], 8);
     }
     mbar_init(&sm->routed, 1);
     sm->abort = 0;
-    sm->n_act = 1;
     sm->act_e[0] = p.E;
-    sm->act_off[0] = 0;
-    sm->act_n[0] = p.T;
-    for (int i = 0; i < p.T; ++i) sm->tok_of_row[i] = i;
     fence_barrier_init();
     tma_prefetch_desc(&map_w1);
     tma_prefetch_desc(&map_w3);
@@ -725,8 +681,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   __syncthreads();
 
   if (warp == kConsumerWarps) {
-    Producer<kFp4> pr(p, &map_w1, &map_w3, &map_w2, sm, ring, lane);
-    pr.run();
+    if (kFp4 || lane == 0) produce<kFp4>(p, &map_w1, &map_w3, &map_w2, sm, ring, lane);
+    __syncwarp();   // lanes without work wait here, not at the CTA's barrier
   } else {
     volatile int* abort = &sm->abort;
     const int G = (int)gridDim.x;
@@ -734,11 +690,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // memory (all indices stay in range), so that they keep meeting at the same barriers.
     // ---------------- phase 1 and 2: routing ----------------
     float* red0 = sm->red[0];
-    if (p.T == 1) gate_partials<1>(p, red0, warp, lane);
-    else if (p.T == 2) gate_partials<2>(p, red0, warp, lane);
-    else if (p.T <= 4) gate_partials<4>(p, red0, warp, lane);
-    else if (p.T <= 8) gate_partials<8>(p, red0, warp, lane);
-    else gate_partials<16>(p, red0, warp, lane);
+    if (p.T == 1)
+      gate_partials<1>(p, 0, red0, warp, lane);
+    else
+      for (int t0 = 0; t0 < p.T; t0 += 4) gate_partials<4>(p, t0, red0, warp, lane);
     __threadfence();
     consumer_sync();
     if (tid == 0) {
@@ -746,7 +701,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       grid_wait(&p.ew->decode_arrive[0], G, abort, p.ew, 404);
     }
     consumer_sync();
-    for (int t = warp; t < p.T; t += kConsumerWarps) select_experts(p, sm, red0 + warp * 512, t, lane);
+    if (warp < p.T) {
+      if (p.E <= 256) select_experts<8>(p, sm, red0 + warp * 512, warp, lane);
+      else select_experts<16>(p, sm, red0 + warp * 512, warp, lane);
+    }
     consumer_sync();
     build_lists(p, sm, tid);
     consumer_sync();
@@ -755,63 +713,103 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int n = p.T * p.k;
       if (tid < n && p.weights_out != nullptr) p.weights_out[tid] = sm->sel_w[tid];
       if (tid < n && p.indices_out != nullptr) p.indices_out[tid] = sm->sel_e[tid];
-      if (p.counts_out != nullptr)
-        for (int e = tid; e < p.E; e += kConsumers) {
-          int c = 0;
-          for (int s = 0; s < n; ++s) c += sm->sel_e[s] == e;
-          p.counts_out[e] = c;
-        }
+      if (p.counts_out != nullptr && tid < p.E) {
+        int c = 0;
+        for (int s = 0; s < n; ++s) c += sm->sel_e[s] == tid;
+        p.counts_out[tid] = c;
+      }
     }
 
     // ---------------- phase 3 and 4: up and down projections ----------------
-    RingPos pos;
-    int buf = 0;
+    int count = 0, buf = 0;      // stages of the tiles so far (the groups take turns)
+    RingPos pos;                 // and where the next one lies
     const uint32_t ring_addr = smem_u32(ring);
-    auto run_tile = [&](auto down_tag, int a, int blk) {
+    const int grp = warp >> 3, w8 = warp & 7, g = lane >> 2, t = lane & 3;
+    const int part = S::kChunk / 8;          // elements of a stage that this warp takes
+    auto run_phase = [&](auto down_tag) {
       constexpr bool kDown = decltype(down_tag)::value;
-      const int K = kDown ? p.I : p.d, n = sm->act_n[a], r0 = sm->act_off[a];
-      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      for (int k0 = 0; k0 < K; k0 += S::kChunk) {
-        const int kw = min(S::kChunk, K - k0);
-        const int off = pos.place(S::bytes(n), p.ring_bytes, nullptr);
-        if (!*abort) mbar_wait(&sm->full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
-        __syncwarp();
-        if (n <= 8) consume_stage<kFp4, kDown, 1>(ring_addr + off, kw, warp, lane, acc, p.ew);
-        else consume_stage<kFp4, kDown, 2>(ring_addr + off, kw, warp, lane, acc, p.ew);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->empty[pos.slot]);
-        pos.next();
-      }
-      float* red = sm->red[buf];
-      buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
-      put_partials(red, warp, lane, acc, n <= 8 ? 1 : 2);
-      consumer_sync();
-      if (kDown) {
-        const int c = tid >> 4, r = tid & 15;
-        if (c < n) p.out[(size_t)(r0 + c) * p.d + blk * 16 + r] = sum_partials(red, c, r);
-      } else {
-        const int c = tid >> 3, f = tid & 7;
-        if (c < n) {
-          const float gate = sum_partials(red, c, f), val = sum_partials(red, c, f + 8);
-          const float w = p.weight_in_expert && a > 0 ? sm->row_w[r0 + c] : 1.f;
-          const int at = kFp4 ? (f < 4 ? 2 * f : 2 * f - 7) : f;   // MXFP4: the octet's order 0 4 1 5 2 6 3 7
-          p.h[(size_t)(r0 + c) * p.I + blk * 8 + at] = __float2bfloat16_rn(swiglu(gate, val, p.swiglu_limit, w));
+      const int K = kDown ? p.I : p.d, nb = kDown ? p.d / 16 : p.I / 8, na = sm->n_act;
+      const int ns = (K + S::kChunk - 1) / S::kChunk;
+      // the warp's next stage, whose token fragments are loaded ahead: tile, stage in it, stages before it
+      TileIter ahead(nb);
+      int ahead_s = (grp ^ count) & 1, ahead_count = count;
+      const __nv_bfloat16* rows[kNT] = {};
+      TokenFrags<kFp4, kNT> cur, nxt;
+      auto rows_of = [&](int a) {
+        const int n = sm->act_n[a], r0 = sm->act_off[a];
+        auto row = [&](int c) -> const __nv_bfloat16* {
+          if (c >= n) return nullptr;
+          return kDown ? p.h + (size_t)(r0 + c) * p.I : p.x + (size_t)sm->tok_of_row[r0 + c] * p.d;
+        };
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) rows[nt] = row(g + 8 * nt);
+      };
+      auto fetch = [&](bool first) {
+        bool moved = first;
+        while (ahead_s >= ns) {          // past the tile's end: the warp's first stage of the next one
+          ahead_count += ns;
+          ahead.next();
+          ahead_s = (grp ^ ahead_count) & 1;
+          moved = true;
+        }
+        if (ahead.a >= na) return;
+        if (moved) rows_of(ahead.a);
+        nxt.template load<kDown>(rows, ahead_s * S::kChunk + w8 * part, K, t);
+        ahead_s += 2;
+      };
+      fetch(true);
+      for (TileIter it(nb); it.a < na; it.next()) {
+        const int n = sm->act_n[it.a], r0 = sm->act_off[it.a];
+        float acc[kNT][4] = {};
+        RingPos mine = pos;
+        if ((grp ^ count) & 1) mine.step(1, p.stages);
+        for (int s = (grp ^ count) & 1; s < ns; s += 2, mine.step(2, p.stages)) {
+          cur = nxt;
+          fetch(false);
+          const int slot = mine.slot;
+          if (!*abort) mbar_wait(&sm->full[slot], mine.phase, abort, p.ew, kDown ? 406 : 405);
+          __syncwarp();
+          if (s * S::kChunk + w8 * part < K) {
+            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(ring_addr + slot * S::kBytes, w8, lane, cur, acc, p.ew);
+            else consume_stage<kFp4, kDown, kNT>(ring_addr + slot * S::kBytes, w8, lane, cur, acc, p.ew);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->empty[slot]);
+        }
+        count += ns;
+        pos.step(ns, p.stages);
+        float* red = sm->red[buf];
+        buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
+        put_partials(red, warp, lane, acc, n <= 8 ? 1 : 2);
+        consumer_sync();
+        if (kDown) {
+          const int c = tid >> 4, r = tid & 15;
+          if (c < n) p.out[(size_t)(r0 + c) * p.d + it.blk * 16 + r] = sum_partials(red, c, r);
+        } else {
+          const int c = tid >> 3, f = tid & 7;
+          if (c < n) {
+            const float gate = sum_partials(red, c, f), val = sum_partials(red, c, f + 8);
+            const float w = p.weight_in_expert && it.a > 0 ? sm->row_w[r0 + c] : 1.f;
+            const int at = kFp4 ? (f < 4 ? 2 * f : 2 * f - 7) : f;   // MXFP4: the octet's order 0 4 1 5 2 6 3 7
+            p.h[(size_t)(r0 + c) * p.I + it.blk * 8 + at] = __float2bfloat16_rn(swiglu(gate, val, p.swiglu_limit, w));
+          }
         }
       }
     };
-    const int nb1 = p.I / 8, nb2 = p.d / 16, na = sm->n_act;
-    for (int j = blockIdx.x; j < na * nb1; j += G) run_tile(std::false_type{}, j / nb1, j % nb1);
-    __threadfence();
-    consumer_sync();
-    if (tid == 0) red_release_add(&p.ew->decode_arrive[1], 1);
-    for (int j = blockIdx.x; j < na * nb2; j += G) run_tile(std::true_type{}, j / nb2, j % nb2);
-    __threadfence();
-    consumer_sync();
-    if (tid == 0) {
-      red_release_add(&p.ew->decode_arrive[2], 1);
-      grid_wait(&p.ew->decode_arrive[2], G, abort, p.ew, 407);
-    }
-    consumer_sync();
+    // all CTAs past a phase before the next reads its rows
+    auto grid_barrier = [&](int which, int site) {
+      __threadfence();
+      consumer_sync();
+      if (tid == 0) {
+        red_release_add(&p.ew->decode_arrive[which], 1);
+        grid_wait(&p.ew->decode_arrive[which], G, abort, p.ew, site);
+      }
+      consumer_sync();
+    };
+    run_phase(std::false_type{});
+    grid_barrier(1, 402);
+    run_phase(std::true_type{});
+    grid_barrier(2, 407);
 
     // ---------------- phase 5: combine, slot order then the shared expert ----------------
     const int d4 = p.d / 4;
@@ -839,6 +837,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
   }
   // the last CTA to get here leaves the grid's counters at zero (nobody waits on them any more)
+  __syncwarp();
   __syncthreads();
   if (tid == 0) {
     __threadfence();
@@ -859,8 +858,14 @@ int decode_gate_splits(int E, int d) {
 cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
                                 bool fp4, int num_sms, cudaStream_t stream) {
   const size_t smem = 227 * 1024;
-  p.ring_bytes = (int)((smem - 1024 - sizeof(DecodeSmem)) / 1024 * 1024);
-  auto kernel = fp4 ? layer_decode_kernel<true> : layer_decode_kernel<false>;
+  const size_t stage = fp4 ? Stage<true>::kBytes : Stage<false>::kBytes;
+  // An even number: a slot then always belongs to the same group of consumer warps, which waits for each of
+  // its fills in turn.  With an odd one the groups would share a slot, and the group of its second fill,
+  // running ahead inside a long tile, would take a first fill that has not landed for its own (a barrier's
+  // parity tells two successive phases apart, not three).
+  p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - sizeof(DecodeSmem)) / stage) & ~1;
+  auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1> : layer_decode_kernel<true, 2>)
+                    : (p.T <= 8 ? layer_decode_kernel<false, 1> : layer_decode_kernel<false, 2>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // no more CTAs than any phase has work for: small layers pay for each arrival at the barriers

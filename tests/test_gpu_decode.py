@@ -123,6 +123,9 @@ CASES = {
     # last k chunk of 128 in the up projection, of 384 in the down projection
     "tails": TINY.replace(T=5, dim=640, inter_dim=384),
     "tails_16": TINY.replace(T=16, dim=1664, inter_dim=896, n_groups=1, n_limited_groups=1, topk=8),
+    # more stages of k in a tile than the weight ring holds, in the up and in the down projection
+    "long_up": TINY.replace(T=2, dim=8192 + 128, n_groups=1, n_limited_groups=1, topk=8),
+    "long_down": TINY.replace(T=2, inter_dim=8192 + 640, n_groups=1, n_limited_groups=1, topk=8),
     # every token on the same few experts: rows of one expert up to T
     "crowded": TINY.replace(T=16, n_groups=1, n_limited_groups=1, topk=8, logit_offset_std=30.0, bias_std=None),
     "no_bias_groups": TINY.replace(T=11, bias_std=None),
@@ -150,6 +153,7 @@ MX_CASES = {
     "mx_16": TINY.replace(T=16, dim=1536, inter_dim=1024, topk=4),
     "mx_crowded": TINY.replace(T=16, dim=512, inter_dim=512, n_groups=1, n_limited_groups=1, topk=8, logit_offset_std=30.0,
                                bias_std=None),
+    "mx_long": TINY.replace(T=3, dim=20480, inter_dim=512, topk=2),
     "mx_clamp_inside": TINY.replace(T=9, dim=512, inter_dim=1536, swiglu_limit=0.05, weight_in_expert=True, w_std=0.1),
 }
 
