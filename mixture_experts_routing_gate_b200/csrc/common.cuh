@@ -19,15 +19,16 @@
 namespace moe {
 
 // ------------------------------------------------------------------------------------------------
-// error word (first 256 bytes of every workspace)
+// control words (first 1024 bytes of every workspace)
 // ------------------------------------------------------------------------------------------------
 struct ErrorWord {
   int status;           // 0 or the first moe_status recorded
   int info;             // the offending value (index, token id, or a wait site)
   int dispatch_ticket;  // dispatch's count of finished histogram blocks (0 between calls)
-  int decode_arrive[3]; // the one-launch layer's grid barriers: CTAs arrived (0 between calls)
+  int decode_arrive[4]; // the one-launch layer's grid counters: logits, up tiles, down, tokens (0 between calls)
   int decode_done;      //   and CTAs finished
-  int pad[57];
+  int decode_ready[144];  // its up tiles finished, per active expert (0 between calls)
+  int pad[104];
 };
 
 __device__ __forceinline__ void record_error(ErrorWord* ew, int status, int info) {

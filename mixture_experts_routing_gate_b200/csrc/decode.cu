@@ -6,29 +6,37 @@
 // What bounds it: the weights of the chosen experts, read once -- every weight meets one to sixteen tokens,
 // far below the flops per byte at which the tensor cores would matter.  So the kernel is a weight stream:
 //
-// * one CTA per SM, all resident at once (cooperative launch), 17 warps: one producer thread keeps TMA copies
-//   of 8 rows x 1 KB in flight into a ring of about 180 KB of shared memory, sixteen consumer warps compute.
-//   At 44 bytes/ns per SM the ring holds 4 us of the stream, more than the memory latency and more than a
-//   grid barrier, so the stream does not stop between the phases: the shared expert's first weights are
-//   loaded while the gate is computed, and the down projection's while the grid finishes the up projection.
-//   Copies of single rows (1 KB) cost about 65 ns each whoever issues them and held the stream at 2 TB/s.
-// * the products run on mma.sync m16n8k16 with the weight rows as the 16-row operand and the tokens as the
-//   8 columns: at most two column tiles, so each weight is read from shared memory once.  The reduction
-//   index is permuted alike for both operands (thread t of a quad holds 8 consecutive elements), so that
-//   a weight fragment is one conflict-free 16-byte shared load from TMA's 128-byte swizzle and a token
-//   fragment one 16-byte load from global memory (L1 or L2; loaded a stage ahead), whatever the token's row.
-//   Eight warps split a stage along k, the two groups of eight take alternate stages; the fp32 accumulators
-//   of a tile are added through shared memory in warp order: nothing depends on scheduling.
-// * an up-projection tile is 8 features: rows 0-7 of the MMA are w1's, rows 8-15 w3's, so gate and value of
-//   a feature meet in one accumulator tile.  A down-projection tile is 16 output features of one expert.
-// * four phases between three grid barriers: partial router logits (K split over the CTAs), then every CTA
-//   selects the experts of all tokens for itself (a few KB from L2; cheaper than another barrier), up
-//   projections into h (bf16 in the workspace), down projections into fp32 rows, combine in slot order.
+// * one CTA per SM, all resident at once (cooperative launch).  One producer warp keeps TMA copies of 8 KB in
+//   flight into a ring of 110 to 200 KB of shared memory, sixteen consumer warps compute.  At 44 bytes/ns per
+//   SM the ring holds about 4 us of the stream, more than the memory latency, so the stream does not stop
+//   between the phases.  (Copies of single rows, 1 KB, cost about 65 ns each whoever issues them and held
+//   the stream at 2 TB/s.)
+// * three router warps turn the logits into the lists of experts while the consumers work on the shared
+//   expert, whose weights need no routing: the selection's latency (it runs once, on code and data that are
+//   not cached) is hidden.
+// * the products run on mma.sync with the weight rows as the 16-row operand and the tokens as the 8 columns
+//   of one or two tiles, so each weight is read from shared memory once.  The reduction index is permuted
+//   alike for both operands (thread t of a quad holds 8 consecutive elements), so that a weight fragment is
+//   one conflict-free shared load from TMA's 128-byte swizzle and a token fragment one 16-byte load from
+//   global memory (L1 or L2; a stage ahead), whatever the token's row.  Eight warps split a stage along k,
+//   the two groups of eight take alternate stages; the accumulators of a tile are added through shared
+//   memory in warp order: nothing depends on scheduling.
+// * in the up projections rows 0-7 of an MMA are w1's and rows 8-15 w3's, so gate and value of a feature meet
+//   in one accumulator tile.  A CTA starts on down-projection tiles of an expert as soon as all of that
+//   expert's h is written (a counter per expert), with no barrier between the projections; CTAs that had one
+//   up tile less take more of the first down tiles.
 //
-// MXFP4 weights: the packed codes and their scales are what travels.  A code's four bits become bf16 by
-// placing sign, exponent and mantissa bits (E2M1 is bf16's format with fewer bits, off by 2^126) and one
-// exact multiply; the block's UE8M0 scale multiplies the fp32 accumulators of its 32 elements, so the
-// weights are exact and the activations keep their bf16 values.
+// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16.
+//
+// MXFP4 weights: what travels is a quarter, so the arithmetic of decoding is what has to be cheap.  The
+// hardware's E2M1 -> f16 conversion takes 73 codes/clock/SM (measured; the stream brings 44), where placing
+// the bits by shifts and logic, 15 operations for 8 codes, takes 34 and bounded the first form of this kernel
+// at 1.4 TB/s.  So the MMAs are f16: the activations of each block of 32 are scaled by a power of two to below
+// 2^15 and held in f16 (exact for bf16 values down to 2^-32 of the block's largest, off by 2^-40 of it
+// below), and the block's scale and the weights' UE8M0 scale multiply the fp32 accumulators of its 32
+// elements.  An up tile is 32 features, one block of h, whose scale its epilogue can therefore choose; tiles
+// are 64 rows, 512 codes of k a stage, so a token fragment serves four MMA row tiles.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -44,40 +52,74 @@ namespace {
 
 constexpr int kConsumerWarps = 16;   // two groups of eight taking alternate stages
 constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kDecThreads = kConsumers + 32;
-constexpr int kMaxStages = 24;
+constexpr int kRouterWarps = 3;
+constexpr int kRouters = kRouterWarps * 32;
+constexpr int kDecThreads = kConsumers + 32 + kRouters;
+constexpr int kMaxStages = 16;
 constexpr int kMaxT = kDecodeMaxTokens;
 constexpr int kMaxS = kMaxT * kMaxRouteTopk;
 constexpr int kMaxAct = kMaxS + 1;  // active experts: the shared one and at most one per slot
-constexpr int kRedPitch = 20;       // floats per token column of the warp-partial exchange (bank = 8 t + g)
-constexpr int kRedFloats = kConsumerWarps * kMaxT * kRedPitch;
+constexpr int kMaxE = 512;
 constexpr int kGateRows = 16;       // router rows per unit of the logit phase
-static_assert(2 * kRedFloats >= kConsumerWarps * 512, "the selection's scores share the exchange buffer");
-static_assert(kMaxT <= 16, "two column tiles of eight tokens");
+constexpr int kGatePitch = 20;      // floats per token column of its exchange (bank = 8 t + g)
+static_assert(kMaxT <= 16, "two column tiles of eight tokens, token masks of 16 bits");
+static_assert(kMaxAct <= sizeof(ErrorWord::decode_ready) / sizeof(int), "a counter for every active expert");
 
+// A stage holds kChunk elements of k of kRows weight rows as two blocks (up: w1's and w3's rows), each as TMA
+// writes a box of 128 bytes x kRows / 2 x kCols in the 128-byte swizzle -- the 16-byte unit u of row r of
+// column c lies at c * (kRows / 2) * 128 + r * 128 + ((u ^ (r & 7)) << 4) -- and, for MXFP4, 16 bytes of
+// scales of each row.
+template <bool kFp4>
+struct Stage {
+  static constexpr int kRowTiles = kFp4 ? 4 : 1;
+  static constexpr int kRows = 16 * kRowTiles;
+  static constexpr int kUp = kRows / 2;                    // features of an up tile
+  static constexpr int kChunk = 512;
+  static constexpr int kCols = kFp4 ? 2 : 8;               // of 256 codes or 64 bf16
+  static constexpr int kColBytes = kRows / 2 * 128;
+  static constexpr int kBlock = kCols * kColBytes;
+  static constexpr int kSOff = 2 * kBlock;
+  static constexpr int kBytes = kSOff + (kFp4 ? kRows * 16 : 0);
+  static constexpr int kRedPitch = kRows + 4;              // floats per token column (bank = 8 t + g)
+  static constexpr int kRedBufs = kFp4 ? 1 : 2;
+};
+
+template <bool kFp4, int kNT>
 struct DecodeSmem {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
   uint64_t routed;                  // the lists below are complete
-  int abort;
+  int abort, last;
+  int up_done;                      // up tiles whose h this CTA has written
   int n_act;                        // active experts, the shared one first
   int sel_e[kMaxS];
   float sel_w[kMaxS];
   int dup[kMaxS];                   // the token already chose this expert in an earlier slot
-  int first[kMaxS], cnt[kMaxS];     // no earlier slot has the expert; its distinct tokens
   int row_of_slot[kMaxS];
   int tok_of_row[kMaxS + kMaxT];
   float row_w[kMaxS + kMaxT];
   int act_e[kMaxAct], act_off[kMaxAct], act_n[kMaxAct];
-  alignas(16) float red[2][kRedFloats];
+  uint32_t mask[kMaxE];             // tokens of each expert
+  int off_of[kMaxE];                // first row of each active expert
+  float bias[kMaxE], offset[kMaxE]; // the router's (zeros where there is none)
+  float scores[kRouterWarps][kMaxE];
+  alignas(16) float red[Stage<kFp4>::kRedBufs][kConsumerWarps * 8 * kNT * Stage<kFp4>::kRedPitch];
 };
 
-// The consumer warps' barrier.  It takes whole warps, so lanes that waited on their own rejoin first.
+// Barriers of whole warps: lanes that waited on their own rejoin first.
 __device__ __forceinline__ void consumer_sync() {
   __syncwarp();
   asm volatile("bar.sync 1, 512;" ::: "memory");
 }
-static_assert(kConsumers == 512, "the named barrier's thread count");
+__device__ __forceinline__ void router_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 2, 96;" ::: "memory");
+}
+__device__ __forceinline__ void writers_sync() {   // the first four consumer warps
+  __syncwarp();
+  asm volatile("bar.sync 3, 128;" ::: "memory");
+}
+static_assert(kConsumers == 512 && kRouters == 96, "the named barriers' thread counts");
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
   int v;
@@ -95,7 +137,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Waits until `*counter` reaches `target` (every CTA of the grid arrived).  Bounded as mbar_wait is.
+// Waits until `*counter` reaches `target`.  Bounded as mbar_wait is.
 __device__ __forceinline__ bool grid_wait(const int* counter, int target, volatile int* abort, ErrorWord* ew, int site) {
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
@@ -111,12 +153,28 @@ __device__ __forceinline__ bool grid_wait(const int* counter, int target, volati
   }
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// A consumer's wait for a stage: the usual, successful test inline; after an abort no waiting at all.
+__device__ __noinline__ void stage_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  if (!*abort) mbar_wait(bar, parity, abort, ew, site);
+}
+__device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  if (!mbar_try_wait(bar, parity)) stage_wait_slow(bar, parity, abort, ew, site);
+  __syncwarp();
+}
+
+template <bool kF16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (kF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -129,22 +187,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-
-// ------------------------------------------------------------------------------------------------
-// stage layout
-// ------------------------------------------------------------------------------------------------
-// A stage holds kChunk elements of k of 16 weight rows: two blocks of 8 rows, each as TMA writes a box of
-// 128 bytes x 8 rows x kBoxes in the 128-byte swizzle -- the 16-byte unit u of row r of box b lies at
-// b * 1024 + r * 128 + ((u ^ r) << 4) -- and, for MXFP4, the rows' scales.
-template <bool kFp4>
-struct Stage {
-  static constexpr int kChunk = kFp4 ? 1024 : 512;
-  static constexpr int kBoxes = kFp4 ? 4 : 8;                  // of 256 codes or 64 bf16
-  static constexpr int kBlock = kBoxes * 1024;
-  static constexpr int kSPitch = kFp4 ? 48 : 0;                // scale rows (32 bytes)
-  static constexpr int kSOff = 2 * kBlock;
-  static constexpr int kBytes = (kSOff + 16 * kSPitch + 1023) & ~1023;
-};
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
 
 struct RingPos {
   int slot = 0;
@@ -154,106 +201,137 @@ struct RingPos {
   }
 };
 
-// Tile j of a phase as (active expert, block of rows), stepped by the grid without a division.
+// The tiles of a CTA as (active expert, block of rows).  Up projections: every gridDim-th tile.  Down
+// projections (early > 0): the `early` first rounds are taken by the CTAs from `first` on alone, which had
+// one up tile less than the others; then every gridDim-th.
 struct TileIter {
-  int j, a, blk, step_a, step_b, nb;
-  __device__ TileIter(int nb_) : j(blockIdx.x), a(j / nb_), blk(j % nb_), step_a(gridDim.x / nb_), step_b(gridDim.x % nb_), nb(nb_) {}
+  int j, a, blk, nb, early, first;
+  __device__ explicit TileIter(int nb_) : nb(nb_), early(0), first(0) { set(blockIdx.x); }
+  __device__ TileIter(int nb_, int early_, int first_) : nb(nb_), early(early_), first(first_) {
+    if (early > 0 && (int)blockIdx.x >= first) {
+      set((int)blockIdx.x - first);
+    } else {
+      const int all = early * ((int)gridDim.x - first);
+      early = 0;
+      set(all + (int)blockIdx.x);
+    }
+  }
+  __device__ void set(int j_) {
+    j = j_;
+    a = j / nb;
+    blk = j - a * nb;
+  }
   __device__ void next() {
-    j += gridDim.x;
-    a += step_a;
-    blk += step_b;
-    if (blk >= nb) {
-      blk -= nb;
-      ++a;
+    const int few = (int)gridDim.x - first;
+    if (early > 1) {
+      --early;
+      set(j + few);
+    } else if (early == 1) {   // j = (early rounds - 1) * few + blockIdx - first
+      early = 0;
+      set(j + few + first);
+    } else {
+      set(j + (int)gridDim.x);
     }
   }
 };
+// The down projections' iterator: CTAs of index >= n_tiles % grid had one up tile less, worth d / I down tiles.
+__device__ __forceinline__ TileIter down_tiles(const DecodeParams& p, int n_act, int nb_up, int nb_down) {
+  const int m = (int)((long)n_act * nb_up % (int)gridDim.x);
+  return TileIter(nb_down, m == 0 ? 0 : (p.d + p.I / 2) / p.I, m);
+}
 
 // ------------------------------------------------------------------------------------------------
 // phase 1: partial router logits
 // ------------------------------------------------------------------------------------------------
-// Sums each of the N values over the warp: halves of the array are exchanged until one value is left
-// per lane (N - 1 shuffles for N <= 32 and a few more), so lane l ends with the sums of values
-// [first, first + max(1, N / 32)).
-template <int N>
-__device__ __forceinline__ int reduce_transposed(float (&v)[N], int lane) {
-  int first = 0;
-  int cnt = N;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    if (cnt > 1) {
-      const int half = cnt / 2;
-      const bool up = (lane & off) != 0;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if (i < half) {
-          const float send = up ? v[i] : v[i + half];
-          const float keep = up ? v[i + half] : v[i];
-          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-        }
-      }
-      first += up ? half : 0;
-      cnt = half;
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-    }
-  }
-  return first;
-}
-
-// Unit u: 16 router rows x one slice of k.  Four warps take 4 rows each, on each quarter of the slice.
-// Tokens t0 to t0 + TT - 1.
-template <int TT>
-__device__ __forceinline__ void gate_partials(const DecodeParams& p, int t0, float* red, int warp, int lane) {
-  const int groups = p.E / kGateRows, units = groups * p.gate_splits;
-  const int nb = p.d / 128;
+// Unit u: 16 router rows x one slice of k, its blocks of 32 dealt to the warps.  The fp32 weights are split
+// exactly into three bf16 parts (hi + mid + lo), whose products with the bf16 activations are exact in fp32.
+template <int kNT>
+__device__ __forceinline__ void gate_partials(const DecodeParams& p, float* red, int warp, int lane) {
+  const int groups = p.E / kGateRows, units = groups * p.gate_splits, nb = p.d / 32;
+  const int g = lane >> 2, t = lane & 3, tid = warp * 32 + lane;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int grp = u % groups, sp = u / groups;
-    const int rsub = warp & 3, ksub = warp >> 2;
-    const int q0 = sp * nb / p.gate_splits, q1 = (sp + 1) * nb / p.gate_splits;
-    const int b0 = q0 + ((q1 - q0) * ksub >> 2), b1 = q0 + ((q1 - q0) * (ksub + 1) >> 2);
-    const int e0 = grp * kGateRows + rsub * 4;
-    float acc[4 * TT];
+    const int b1 = (sp + 1) * nb / p.gate_splits;
+    const float* w0 = p.w_gate + (size_t)(grp * kGateRows + g) * p.d + t * 8;
+    float acc[kNT][4] = {};
+    for (int b = sp * nb / p.gate_splits + warp; b < b1; b += kConsumerWarps) {
+      float w[2][8];
+      uint4 x[kNT];
 #pragma unroll
-    for (int i = 0; i < 4 * TT; ++i) acc[i] = 0.f;
-#pragma unroll 2
-    for (int b = b0; b < b1; ++b) {
-      const int k = b * 128 + lane * 4;
-      float4 w[4];
+      for (int r = 0; r < 2; ++r) {
+        const float4* src = reinterpret_cast<const float4*>(w0 + (size_t)r * 8 * p.d + b * 32);
+        *reinterpret_cast<float4*>(&w[r][0]) = __ldg(src);
+        *reinterpret_cast<float4*>(&w[r][4]) = __ldg(src + 1);
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) w[r] = __ldg(reinterpret_cast<const float4*>(p.w_gate + (size_t)(e0 + r) * p.d + k));
+      for (int nt = 0; nt < kNT; ++nt)
+        x[nt] = g + 8 * nt < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(g + 8 * nt) * p.d + b * 32 + t * 8))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+      for (int plane = 0; plane < 3; ++plane) {
+        uint32_t a[2][4];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if (t0 + t < p.T) {
-          const uint2 xv = __ldg(reinterpret_cast<const uint2*>(p.x + (size_t)(t0 + t) * p.d + k));
-          const float x0 = __uint_as_float(xv.x << 16), x1 = __uint_as_float(xv.x & 0xffff0000u);
-          const float x2 = __uint_as_float(xv.y << 16), x3 = __uint_as_float(xv.y & 0xffff0000u);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float a = acc[t * 4 + r];
-            a = fmaf(w[r].x, x0, a);
-            a = fmaf(w[r].y, x1, a);
-            a = fmaf(w[r].z, x2, a);
-            acc[t * 4 + r] = fmaf(w[r].w, x3, a);
+          for (int i = 0; i < 4; ++i) {
+            a[r][i] = bf16x2_bits(w[r][2 * i], w[r][2 * i + 1]);
+            w[r][2 * i] -= __uint_as_float(a[r][i] << 16);
+            w[r][2 * i + 1] -= __uint_as_float(a[r][i] & 0xffff0000u);
           }
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          mma_16816<false>(acc[nt], a[0][0], a[1][0], a[0][1], a[1][1], x[nt].x, x[nt].y);
+          mma_16816<false>(acc[nt], a[0][2], a[1][2], a[0][3], a[1][3], x[nt].z, x[nt].w);
         }
       }
     }
-    const int first = reduce_transposed<4 * TT>(acc, lane);
-    constexpr int kPer = 4 * TT > 32 ? 4 * TT / 32 : 1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) red[warp * 64 + first + i] = acc[i];   // lanes with equal `first` agree
-    consumer_sync();
-    const int tid = warp * 32 + lane;
-    if (tid < kGateRows * TT) {
-      const int t = tid / kGateRows, row = tid % kGateRows;
-      if (t0 + t < p.T) {
-        const int at = (row >> 2) * 64 + t * 4 + (row & 3);
-        p.partial[((size_t)sp * p.T + t0 + t) * p.E + grp * kGateRows + row] =
-            (red[at] + red[at + 4 * 64]) + (red[at + 8 * 64] + red[at + 12 * 64]);
-      }
+    for (int nt = 0; nt < kNT; ++nt) {
+      float* c = red + (warp * 8 * kNT + nt * 8 + 2 * t) * kGatePitch + g;
+      c[0] = acc[nt][0];
+      c[kGatePitch] = acc[nt][1];
+      c[8] = acc[nt][2];
+      c[kGatePitch + 8] = acc[nt][3];
     }
     consumer_sync();
+    const int c = tid >> 4, r = tid & 15;
+    if (c < p.T) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kConsumerWarps; ++i) v += red[(i * 8 * kNT + c) * kGatePitch + r];
+      p.partial[((size_t)sp * p.T + c) * p.E + grp * kGateRows + r] = v;
+    }
+    consumer_sync();
+  }
+}
+
+// The power of two that brings a block whose largest magnitude has the biased exponent eb below 2^15, and its
+// inverse.  (Zero, tiny and infinite blocks included: eb is at least 15, and 255 leaves infinities and NaN.)
+__device__ __forceinline__ float block_up(int eb) { return __uint_as_float((uint32_t)(268 - max(eb, 15)) << 23); }
+__device__ __forceinline__ float block_down(int eb) { return __uint_as_float((uint32_t)(max(eb, 15) - 14) << 23); }
+
+// x in f16 blocks of 32 with their scales (MXFP4), spread over the grid.
+__device__ __forceinline__ void scale_tokens(const DecodeParams& p, int tid) {
+  const int n = p.T * p.d / 8;   // a multiple of 4: the four threads of a block are all in
+  for (int i = blockIdx.x * kConsumers + tid; i < n; i += gridDim.x * kConsumers) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.x) + i);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(q[j] & 0x7fffu, (q[j] >> 16) & 0x7fffu));
+    const uint32_t group = 0xfu << (threadIdx.x & 28);
+    m = max(m, __shfl_xor_sync(group, m, 1));
+    m = max(m, __shfl_xor_sync(group, m, 2));
+    const int eb = (int)(m >> 7);
+    const float up = block_up(eb);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 r = __floats2half2_rn(__uint_as_float(q[j] << 16) * up, __uint_as_float(q[j] & 0xffff0000u) * up);
+      h[j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    reinterpret_cast<uint4*>(p.x16)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+    if ((i & 3) == 0) p.x_scale[i >> 2] = block_down(eb);
   }
 }
 
@@ -272,23 +350,42 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return max((b & 0x80000000u) ? ~b : b | 0x80000000u, 1u);
 }
 
-template <int PL>   // experts per lane: e = lane + 32 i
-__device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem* sm, float* scores, int t, int lane) {
+// Lane l holds experts 128 q + 4 l + r as i = 4 q + r, ascending in i.
+template <int PL>
+__device__ __forceinline__ void select_experts(const DecodeParams& p, const float* bias, const float* offset, int* sel_e,
+                                               float* sel_w, float* scores, int t, int lane) {
+  auto expert = [&](int i) { return (i >> 2) * 128 + 4 * lane + (i & 3); };
   float sc[PL];
   uint32_t key[PL];
+  // the partial logits of up to eight slices in one round of loads: under the weight stream a round takes
+  // about 2 us
+  constexpr int kRound = 32 / PL * 2;
 #pragma unroll
   for (int i = 0; i < PL; ++i) sc[i] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < p.gate_splits; ++s) {
-    const float* src = p.partial + ((size_t)s * p.T + t) * p.E;
+  for (int s0 = 0; s0 < p.gate_splits; s0 += kRound) {
+    float4 v[kRound][PL / 4];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) sc[i] += __ldcg(src + min(lane + 32 * i, p.E - 1));
+    for (int s = 0; s < kRound; ++s)
+#pragma unroll
+      for (int q = 0; q < PL / 4; ++q) {
+        v[s][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 + s < p.gate_splits && expert(4 * q) < p.E)
+          v[s][q] = __ldcg(reinterpret_cast<const float4*>(p.partial + ((size_t)(s0 + s) * p.T + t) * p.E + expert(4 * q)));
+      }
+#pragma unroll
+    for (int s = 0; s < kRound; ++s)
+#pragma unroll
+      for (int q = 0; q < PL / 4; ++q) {
+        sc[4 * q] += v[s][q].x;
+        sc[4 * q + 1] += v[s][q].y;
+        sc[4 * q + 2] += v[s][q].z;
+        sc[4 * q + 3] += v[s][q].w;
+      }
   }
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int e = lane + 32 * i;
-    if (p.logit_offset != nullptr) sc[i] += __ldg(p.logit_offset + min(e, p.E - 1));
-    if (e >= p.E) sc[i] = -INFINITY;
+    const int e = expert(i);
+    sc[i] = e < p.E ? sc[i] + offset[e] : -INFINITY;
   }
   if (p.score_func == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY, z = 0.f;
@@ -297,7 +394,7 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      sc[i] = lane + 32 * i < p.E ? expf(sc[i] - m) : 0.f;
+      sc[i] = expert(i) < p.E ? expf(sc[i] - m) : 0.f;
       z += sc[i];
     }
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -306,7 +403,7 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
   } else {
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (lane + 32 * i < p.E) sc[i] = affinity_rn(sc[i], p.score_func);
+      if (expert(i) < p.E) sc[i] = affinity_rn(sc[i], p.score_func);
   }
 
   int my_e = 0;          // lane j holds slot j's expert and unbiased score
@@ -326,14 +423,14 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (lane + 32 * i < p.E) scores[lane + 32 * i] = sc[i];
+      if (expert(i) < p.E) scores[expert(i)] = sc[i];
     __syncwarp();
     my_s = scores[my_e];
   } else {
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = lane + 32 * i;
-      const float b = e < p.E ? __fadd_rn(sc[i], p.bias != nullptr ? p.bias[e] : 0.f) : 0.f;
+      const int e = expert(i);
+      const float b = e < p.E ? __fadd_rn(sc[i], bias[e]) : 0.f;
       if (e < p.E) scores[e] = b;
       key[i] = e < p.E ? order_key(b) : 0u;
     }
@@ -367,7 +464,7 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
       const uint32_t kept = __ballot_sync(0xffffffffu, grp < p.G && better < p.g);
 #pragma unroll
       for (int i = 0; i < PL; ++i) {
-        const int e = lane + 32 * i;
+        const int e = expert(i);
         if (e < p.E && !((kept >> ((e / per) * L)) & 1u)) key[i] = 0u;
       }
     }
@@ -379,7 +476,7 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
       for (int i = 0; i < PL; ++i)
         if (key[i] > best) {
           best = key[i];
-          at = lane + 32 * i;
+          at = expert(i);
         }
       const uint32_t top = __reduce_max_sync(0xffffffffu, best);
       const int e = __reduce_min_sync(0xffffffffu, top != 0u && best == top ? at : 0x7fffffff);
@@ -387,11 +484,11 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
       float mine = 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i)
-        if (lane + 32 * i == ec) {
+        if (expert(i) == ec) {
           mine = sc[i];
           key[i] = 0u;
         }
-      const float s = __shfl_sync(0xffffffffu, mine, ec & 31);
+      const float s = __shfl_sync(0xffffffffu, mine, (ec & 127) >> 2);
       if (lane == j) {
         my_e = ec;
         my_s = s;
@@ -404,134 +501,197 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, DecodeSmem
     float w = my_s;
     if (p.renorm) w = __fdiv_rn(w, total);
     w = __fmul_rn(w, p.route_scale);
-    sm->sel_e[t * p.k + lane] = my_e;
-    sm->sel_w[t * p.k + lane] = w;
+    sel_e[t * p.k + lane] = my_e;
+    sel_w[t * p.k + lane] = w;
   }
 }
 
-// The lists of active experts and their token rows, by the consumer threads (at most 128 slots).  Active
-// expert 0 is the shared one with every token; the routed ones follow in the order of their first slot.
-// A token that names an expert twice (a table may) has one row there.
-__device__ __forceinline__ void build_lists(const DecodeParams& p, DecodeSmem* sm, int tid) {
+// The lists of active experts and their token rows, by the router warps.  Active expert 0 is the shared one
+// with every token, the routed ones follow by index; an expert's rows are its tokens in order.  A token that
+// names an expert twice (a table may) has one row there.  sm->mask is zero on entry and on exit.
+template <typename Smem>
+__device__ __forceinline__ void build_lists(const DecodeParams& p, Smem* sm, int rt, int lane) {
   const int S = p.T * p.k;
-  const bool live = tid < S;
-  const int t = live ? tid / p.k : 0, e = live ? sm->sel_e[tid] : -1;
-  if (live) {
+  for (int s = rt; s < S; s += kRouters) {
+    const int e = sm->sel_e[s], t = s / p.k;
     int d = 0;
-    for (int s = t * p.k; s < tid; ++s) d |= sm->sel_e[s] == e;
-    sm->dup[tid] = d;
+    for (int q = t * p.k; q < s; ++q) d |= sm->sel_e[q] == e;
+    sm->dup[s] = d;
+    atomicOr(&sm->mask[e], 1u << t);
   }
-  consumer_sync();
-  int n = 0, rank = 0, s0 = tid;
-  float wsum = 0.f;
-  if (live) {
-    for (int s = S - 1; s >= 0; --s) {
-      if (sm->sel_e[s] != e) continue;
-      s0 = s < s0 ? s : s0;
-      if (!sm->dup[s]) {
-        ++n;
-        rank += s < t * p.k;
+  router_sync();
+  if (rt < 32) {
+    // lane l: experts [l per, (l + 1) per): how many are active (high half) and their rows (low half)
+    const int per = (p.E + 31) / 32, e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) {
+      const uint32_t m = sm->mask[e];
+      mine += m != 0u ? 0x10000 + __popc(m) : 0;
+    }
+    int run = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) sm->n_act = 1 + (run >> 16);
+    run -= mine;
+    for (int e = e0; e < e1; ++e) {
+      const uint32_t m = sm->mask[e];
+      if (m != 0u) {
+        const int a = 1 + (run >> 16), off = p.T + (run & 0xffff);
+        sm->act_e[a] = e;
+        sm->act_n[a] = __popc(m);
+        sm->act_off[a] = off;
+        sm->off_of[e] = off;
+        run += 0x10000 + __popc(m);
       }
     }
-    for (int s = t * p.k; s < (t + 1) * p.k; ++s)
-      if (sm->sel_e[s] == e) wsum += sm->sel_w[s];
-    sm->first[tid] = s0 == tid;
-    sm->cnt[tid] = n;
   }
-  consumer_sync();
-  if (live) {
-    int order = 1, off = p.T;
-    for (int s = 0; s < s0; ++s)
-      if (sm->first[s]) {
-        ++order;
-        off += sm->cnt[s];
-      }
-    const int row = off + rank;
-    sm->row_of_slot[tid] = row;
-    if (!sm->dup[tid]) {
+  router_sync();
+  for (int s = rt; s < S; s += kRouters) {
+    const int e = sm->sel_e[s], t = s / p.k;
+    const int row = sm->off_of[e] + __popc(sm->mask[e] & ((1u << t) - 1u));
+    sm->row_of_slot[s] = row;
+    if (!sm->dup[s]) {
+      float w = 0.f;
+      for (int q = t * p.k; q < (t + 1) * p.k; ++q)
+        if (sm->sel_e[q] == e) w += sm->sel_w[q];
       sm->tok_of_row[row] = t;
-      sm->row_w[row] = wsum;
+      sm->row_w[row] = w;
     }
-    if (s0 == tid) {
-      sm->act_e[order] = e;
-      sm->act_off[order] = off;
-      sm->act_n[order] = n;
+  }
+  router_sync();
+  for (int s = rt; s < S; s += kRouters) sm->mask[sm->sel_e[s]] = 0u;
+  router_sync();
+}
+
+// The router warps: selection and lists, then the CTA's reports of finished up tiles.
+//
+// A round trip to L2 takes about 2 us under the weight stream, so up to three tokens are selected by every CTA
+// for itself, one per warp, from the partial logits of the whole grid.  More tokens are dealt to the first
+// CTAs, one each, and their choices read back after one more counter: 16 tokens 6 a warp took 34 us.
+template <bool kFp4, typename Smem>
+__device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, int lane) {
+  volatile int* abort = &sm->abort;
+  const int rt = rw * 32 + lane, S = p.T * p.k;
+  const bool dealt = p.T > kRouterWarps && (int)gridDim.x >= p.T;
+  for (int e = rt; e < p.E; e += kRouters) {
+    sm->bias[e] = p.bias != nullptr ? p.bias[e] : 0.f;
+    sm->offset[e] = p.logit_offset != nullptr ? p.logit_offset[e] : 0.f;
+  }
+  router_sync();
+  auto select = [&](int t) {
+    if (p.E <= 256) select_experts<8>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, lane);
+    else select_experts<16>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, lane);
+  };
+  if (lane == 0) grid_wait(&p.ew->decode_arrive[0], (int)gridDim.x, abort, p.ew, 404);
+  __syncwarp();
+  if (!dealt) {
+    for (int t = rw; t < p.T; t += kRouterWarps) select(t);
+  } else {
+    if (rw == 0 && (int)blockIdx.x < p.T) {
+      const int t = blockIdx.x;
+      select(t);
+      __syncwarp();
+      if (lane < p.k) {
+        p.route_e[t * p.k + lane] = sm->sel_e[t * p.k + lane];
+        p.route_w[t * p.k + lane] = sm->sel_w[t * p.k + lane];
+      }
+      __syncwarp();
+      if (lane == 0) red_release_add(&p.ew->decode_arrive[3], 1);
     }
-  } else if (tid == kConsumers - 1) {
-    int c = 1;
-    for (int s = 0; s < S; ++s) c += sm->first[s];
-    sm->n_act = c;
-    sm->act_e[0] = p.E;
-    sm->act_off[0] = 0;
-    sm->act_n[0] = p.T;
-  } else if (tid >= kMaxS && tid < kMaxS + p.T) {
-    sm->tok_of_row[tid - kMaxS] = tid - kMaxS;
-    sm->row_w[tid - kMaxS] = 1.f;
+    router_sync();
+    if (lane == 0) grid_wait(&p.ew->decode_arrive[3], p.T, abort, p.ew, 410);
+    __syncwarp();
+    for (int s = rt; s < S; s += kRouters) {
+      sm->sel_e[s] = *abort ? 0 : __ldcg(p.route_e + s);   // after an abort the scratch may hold anything
+      sm->sel_w[s] = __ldcg(p.route_w + s);
+    }
+  }
+  router_sync();
+  build_lists(p, sm, rt, lane);
+  if (rt == 0) mbar_arrive(&sm->routed);
+  if (blockIdx.x == 0) {
+    for (int s = rt; s < S; s += kRouters) {
+      if (p.weights_out != nullptr) p.weights_out[s] = sm->sel_w[s];
+      if (p.indices_out != nullptr) p.indices_out[s] = sm->sel_e[s];
+    }
+    if (p.counts_out != nullptr)
+      for (int e = rt; e < p.E; e += kRouters) {
+        int c = 0;
+        for (int s = 0; s < S; ++s) c += sm->sel_e[s] == e;
+        p.counts_out[e] = c;
+      }
+  }
+  // Reports of finished up tiles, kept off the consumers' path: a release at GPU scope waits for the writes
+  // before it, 1 to 2 us under the stream.
+  if (rt == 0) {
+    const int nb = p.I / Stage<kFp4>::kUp;
+    const long long t0 = clock64();
+    int seen = 0;
+    for (TileIter it(nb); it.a < sm->n_act;) {
+      const int done = *(volatile int*)&sm->up_done;
+      if (done == seen) {
+        __nanosleep(100);
+        if (*abort || clock64() - t0 > 2 * kWaitLimitCycles) break;
+        continue;
+      }
+      __threadfence();
+      atomicAdd(&p.ew->decode_arrive[1], done - seen);
+      for (; seen < done; ++seen, it.next()) atomicAdd(&p.ew->decode_ready[it.a], 1);
+    }
   }
 }
-static_assert(kMaxS + kMaxT < kConsumers - 1, "the list threads do not overlap");
 
 // ------------------------------------------------------------------------------------------------
 // consumers: one stage into the warp's accumulators
 // ------------------------------------------------------------------------------------------------
-// Four bf16 pairs of the eight E2M1 codes of w, pair i holding codes i and i + 4: the sign bit to bit
-// 15, exponent and mantissa to bits 8-6, which is the value times 2^-126 (subnormals included), then an
-// exact multiply by 2^126.
-__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&v)[4]) {
-  const uint32_t k126 = 0x7E807E80u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t y = w << (12 - 4 * i);
-    const uint32_t b = (y & 0x80008000u) | ((y >> 6) & 0x01C001C0u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&k126));
-    v[i] = *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
-
-// Block scales in [2, 252]; others are clamped and reported.
-__device__ __forceinline__ uint32_t checked_scales(uint32_t s4, ErrorWord* ew) {
-  if (__vminu4(s4, 0xFCFCFCFCu) != s4 || __vmaxu4(s4, 0x02020202u) != s4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t s = (s4 >> (8 * i)) & 0xFFu;
-      if (s < 2u || s > 252u) record_error(ew, MOE_ERR_DEVICE, 0x10000 + (int)s);
-    }
-    s4 = __vmaxu4(__vminu4(s4, 0xFCFCFCFCu), 0x02020202u);
-  }
-  return s4;
-}
-
-// The warp's token fragments of one stage: 16 bytes of each of its kBlocks blocks of 32 elements, for
-// token columns g and g + 8.
+// The warp's 64 elements of a stage's token rows (rows g and g + 8 of the tile's): two blocks of 32, of which
+// thread t holds 8 elements each; MXFP4: and the blocks' scales of the token columns 2t, 2t + 1 (+ 8).
 template <bool kFp4, int kNT>
 struct TokenFrags {
-  static constexpr int kBlocks = kFp4 ? 4 : 2;
-  uint4 v[kNT][kBlocks];
-  // row: the columns' rows or null; k: first element of the warp's part, K: elements of a row
-  template <bool kDown>
-  __device__ __forceinline__ void load(const __nv_bfloat16* const (&row)[kNT], int k, int K, int t) {
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int kb = 0; kb < kBlocks; ++kb) {
-        v[nt][kb] = make_uint4(0u, 0u, 0u, 0u);
-        if (k < K && row[nt] != nullptr) {
-          const uint4* at = reinterpret_cast<const uint4*>(row[nt] + k + kb * 32 + t * 8);
-          v[nt][kb] = kDown ? __ldcg(at) : __ldg(at);   // h is written during this kernel: read from L2
-        }
-      }
-  }
+  uint4 v[kNT][2];
+  float2 scale[kFp4 ? kNT : 1][2];   // .x, .y: the two blocks; of columns 2t and 2t + 1
 };
 
-// kPaired: the token rows already hold each octet in the order 0 4 1 5 2 6 3 7 (MXFP4's h).
-// w: the warp's place in its group of eight.
-template <bool kFp4, bool kPaired, int NT, int kNT>
+// Four f16 pairs of the eight E2M1 codes of w.
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+
+// Whether some of four block scales may lie outside [2, 252] (bytes below 2, or whose complement is below 3).
+__device__ __forceinline__ uint32_t scales_outside(uint32_t s) {
+  return (((s - 0x02020202u) & ~s) | ((~s - 0x03030303u) & s)) & 0x80808080u;
+}
+// Those clamped and reported.
+__device__ __noinline__ uint32_t clamp_scales(uint32_t s4, ErrorWord* ew) {
+  uint32_t r = 0u;
+  for (int i = 0; i < 32; i += 8) {
+    uint32_t s = (s4 >> i) & 0xFFu;
+    if (s < 2u || s > 252u) {
+      record_error(ew, MOE_ERR_DEVICE, 0x10000 + (int)s);
+      s = s < 2u ? 2u : 252u;
+    }
+    r |= s << i;
+  }
+  return r;
+}
+
+// w: the warp's place in its group of eight, which takes elements [64 w, 64 w + 64) of the stage.
+template <bool kFp4, bool kDown, int NT, int kNT>
 __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT>& tok,
-                                              float (&acc)[kNT][4], ErrorWord* ew) {
+                                              float (&acc)[Stage<kFp4>::kRowTiles][kNT][4], ErrorWord* ew) {
   using S = Stage<kFp4>;
   const int g = lane >> 2, t = lane & 3;
-  if (!kFp4) {
-    const uint32_t wr = stage + w * 1024 + g * 128;   // the warp's 64 elements are box w
+  if constexpr (!kFp4) {
+    const uint32_t wr = stage + w * S::kColBytes + g * 128;   // the warp's elements are column w
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const uint32_t at = wr + (((kb * 4 + t) ^ g) << 4);
@@ -539,105 +699,125 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, c
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 b = tok.v[nt][kb];
-        mma_bf16(acc[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-        mma_bf16(acc[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        mma_16816<false>(acc[0][nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+        mma_16816<false>(acc[0][nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
       }
     }
   } else {
-    // the warp's 128 elements are half of box w / 2
-    const uint32_t wr = stage + (w >> 1) * 1024 + g * 128 + t * 4, sr = stage + S::kSOff + g * S::kSPitch + w * 4;
-    const uint32_t s_lo = checked_scales(lds32(sr), ew), s_hi = checked_scales(lds32(sr + 8 * S::kSPitch), ew);
+    // row tile i: rows 8 i + g of both blocks (up), or rows 16 i + g and 16 i + 8 + g (down)
+    constexpr int kHi = kDown ? 8 : S::kRows / 2;                 // from a low row to its high row, in scale rows
+    constexpr uint32_t kHiBytes = kDown ? 8 * 128 : S::kBlock;
+    uint32_t sc[S::kRowTiles], bad = 0u;
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-      const uint32_t at = wr + ((((w & 1) * 4 + kb) ^ g) << 4);
-      uint32_t lo[4], hi[4];
-      e2m1_pairs(lds32(at), lo);
-      e2m1_pairs(lds32(at + S::kBlock), hi);
-      const float f_lo = __uint_as_float(((s_lo >> (8 * kb)) & 0xFFu) << 23);
-      const float f_hi = __uint_as_float(((s_hi >> (8 * kb)) & 0xFFu) << 23);
+    for (int i = 0; i < S::kRowTiles; ++i) {
+      const uint32_t at = stage + S::kSOff + ((kDown ? 16 : 8) * i + g) * 16 + w * 2;
+      sc[i] = lds16(at) | (lds16(at + kHi * 16) << 16);
+      bad |= scales_outside(sc[i]);
+    }
+    if (bad != 0u) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint4 b = tok.v[nt][kb];
-        if (!kPaired)
-          b = make_uint4(__byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632), __byte_perm(b.y, b.w, 0x5410),
-                         __byte_perm(b.y, b.w, 0x7632));
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_bf16(part, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-        mma_bf16(part, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-        acc[nt][0] = fmaf(part[0], f_lo, acc[nt][0]);
-        acc[nt][1] = fmaf(part[1], f_lo, acc[nt][1]);
-        acc[nt][2] = fmaf(part[2], f_hi, acc[nt][2]);
-        acc[nt][3] = fmaf(part[3], f_hi, acc[nt][3]);
+      for (int i = 0; i < S::kRowTiles; ++i) sc[i] = clamp_scales(sc[i], ew);
+    }
+    const uint32_t col = stage + (w >> 2) * S::kColBytes + g * 128 + t * 4;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const uint32_t unit = ((2 * (w & 3) + kb) ^ g) << 4;
+#pragma unroll
+      for (int i = 0; i < S::kRowTiles; ++i) {
+        const uint32_t at = col + unit + (kDown ? (i >> 1) * S::kBlock + (i & 1) * 16 * 128 : i * 8 * 128);
+        uint32_t lo[4], hi[4];
+        e2m1_to_f16(lds32(at), lo);
+        e2m1_to_f16(lds32(at + kHiBytes), hi);
+        const float f_lo = __uint_as_float((kb == 0 ? sc[i] << 23 : sc[i] << 15) & 0x7f800000u);
+        const float f_hi = __uint_as_float((kb == 0 ? sc[i] << 7 : sc[i] >> 1) & 0x7f800000u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 b = tok.v[nt][kb];
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16816<true>(part, lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+          mma_16816<true>(part, lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+          const float s0 = kb == 0 ? tok.scale[nt][0].x : tok.scale[nt][0].y;
+          const float s1 = kb == 0 ? tok.scale[nt][1].x : tok.scale[nt][1].y;
+          acc[i][nt][0] = fmaf(part[0] * s0, f_lo, acc[i][nt][0]);
+          acc[i][nt][1] = fmaf(part[1] * s1, f_lo, acc[i][nt][1]);
+          acc[i][nt][2] = fmaf(part[2] * s0, f_hi, acc[i][nt][2]);
+          acc[i][nt][3] = fmaf(part[3] * s1, f_hi, acc[i][nt][3]);
+        }
       }
     }
   }
 }
 
-// The warp's accumulators of a tile into the exchange buffer, [warp][token column][kRedPitch rows].
-template <int kNT>
-__device__ __forceinline__ void put_partials(float* red, int warp, int lane, const float (&acc)[kNT][4], int nt_used) {
+// The warp's accumulators of a tile into the exchange buffer, [warp][token column][row].
+template <bool kFp4, int kNT>
+__device__ __forceinline__ void put_partials(float* red, int warp, int lane,
+                                             const float (&acc)[Stage<kFp4>::kRowTiles][kNT][4], int nt_used) {
+  using S = Stage<kFp4>;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
     if (nt >= nt_used) break;
-    float* c = red + (warp * kMaxT + nt * 8 + 2 * t) * kRedPitch + g;
-    c[0] = acc[nt][0];
-    c[kRedPitch] = acc[nt][1];
-    c[8] = acc[nt][2];
-    c[kRedPitch + 8] = acc[nt][3];
+#pragma unroll
+    for (int i = 0; i < S::kRowTiles; ++i) {
+      float* c = red + (warp * 8 * kNT + nt * 8 + 2 * t) * S::kRedPitch + i * 16 + g;
+      c[0] = acc[i][nt][0];
+      c[S::kRedPitch] = acc[i][nt][1];
+      c[8] = acc[i][nt][2];
+      c[S::kRedPitch + 8] = acc[i][nt][3];
+    }
   }
 }
+template <bool kFp4, int kNT>
 __device__ __forceinline__ float sum_partials(const float* red, int col, int row) {
   float v = 0.f;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) v += red[(w * kMaxT + col) * kRedPitch + row];
+  for (int w = 0; w < kConsumerWarps; ++w) v += red[(w * 8 * kNT + col) * Stage<kFp4>::kRedPitch + row];
   return v;
 }
 
 // ------------------------------------------------------------------------------------------------
-// the kernel
+// the weight stream: TMA copies by lane 0 and, for MXFP4, the scales by cp.async of all 32 lanes (then the
+// full barriers count their 32 arrivals too)
 // ------------------------------------------------------------------------------------------------
-// The weight stream: TMA copies by lane 0 and, for MXFP4, the scales by cp.async of all 32 lanes (then the
-// full barriers count their 32 arrivals too).
-template <bool kFp4>
+template <bool kFp4, typename Smem>
 __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap* map_w1, const CUtensorMap* map_w3,
-                                        const CUtensorMap* map_w2, DecodeSmem* sm, uint8_t* ring, int lane) {
+                                        const CUtensorMap* map_w2, Smem* sm, uint8_t* ring, int lane) {
   using S = Stage<kFp4>;
   if (p.test_stall) return;
   volatile int* abort = &sm->abort;
-  constexpr int kBox = kFp4 ? 256 : 64;
+  constexpr int kColElems = S::kChunk / S::kCols;
   RingPos pos;
   int issued = 0;
   bool ok = true, routed = false;
-  auto tile = [&](bool down, int a, int blk) {
-    const int K = down ? p.I : p.d, e = sm->act_e[a];
-    const int row = down ? e * p.d + blk * 16 : e * p.I + blk * 8;
+  auto tile = [&](bool down, int e, int blk) {
+    const int K = down ? p.I : p.d;
+    const int row = down ? e * p.d + blk * S::kRows : e * p.I + blk * S::kUp;
     const CUtensorMap *m0 = down ? map_w2 : map_w1, *m1 = down ? map_w2 : map_w3;
+    const int row1 = down ? row + S::kRows / 2 : row;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
       uint64_t* bar = &sm->full[pos.slot];
       uint8_t* dst = ring + pos.slot * S::kBytes;
       if (kFp4) {
         if (!mbar_wait_warp(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
-        const int r = lane >> 1, half = lane & 1;
-        const uint8_t* ws = down ? p.w2s : (r < 8 ? p.w1s : p.w3s);
-        if (k0 + half * 512 < K)
-          cp_async16(smem_u32(dst + S::kSOff + r * S::kSPitch + half * 16),
-                     ws + ((size_t)(row + (down ? r : r & 7)) * K + k0) / 32 + half * 16);
+        const uint8_t* s0 = down ? p.w2s : p.w1s;
+        const uint8_t* s1 = down ? p.w2s : p.w3s;
+        cp_async16(smem_u32(dst + S::kSOff + lane * 16), s0 + ((size_t)(row + lane) * K + k0) / 32);
+        cp_async16(smem_u32(dst + S::kSOff + (32 + lane) * 16), s1 + ((size_t)(row1 + lane) * K + k0) / 32);
         cp_async_arrive(bar);
-      } else if (lane == 0) {
-        if (!mbar_wait(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
+      } else if (!mbar_wait(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) {
+        return false;
       }
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, 2 * S::kBlock);   // whole boxes: what lies past K is filled with zeros
-        tma_load_3d(dst, m0, bar, 0, row, k0 / kBox);
-        tma_load_3d(dst + S::kBlock, m1, bar, 0, down ? row + 8 : row, k0 / kBox);
+        tma_load_3d(dst, m0, bar, 0, row, k0 / kColElems);
+        tma_load_3d(dst + S::kBlock, m1, bar, 0, row1, k0 / kColElems);
       }
       ++issued;
       pos.step(1, p.stages);
     }
     return true;
   };
-  const int nb1 = p.I / 8, nb2 = p.d / 16;
+  const int nb1 = p.I / S::kUp, nb2 = p.d / S::kRows;
   for (TileIter it(nb1); ok; it.next()) {
     if (it.a > 0 && !routed) {
       ok = kFp4 ? mbar_wait_warp(&sm->routed, 0, abort, p.ew, 403) : mbar_wait(&sm->routed, 0, abort, p.ew, 403);
@@ -645,173 +825,238 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
       if (!ok) break;
     }
     if (routed && it.a >= sm->n_act) break;
-    ok = tile(false, it.a, it.blk);
+    ok = tile(false, it.a == 0 ? p.E : sm->act_e[it.a], it.blk);
   }
   if (ok)
-    for (TileIter it(nb2); ok && it.a < sm->n_act; it.next()) ok = tile(true, it.a, it.blk);
+    for (TileIter it = down_tiles(p, sm->n_act, nb1, nb2); ok && it.a < sm->n_act; it.next())
+      ok = tile(true, it.a == 0 ? p.E : sm->act_e[it.a], it.blk);
   if (!ok) {   // let every copy already issued land before the CTA leaves
     for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
       mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// the kernel
+// ------------------------------------------------------------------------------------------------
 // kNT: column tiles of eight tokens (1 for batches of at most 8, whose fragments then take half the registers).
 template <bool kFp4, int kNT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     layer_decode_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w3,
                         const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ DecodeParams p) {
   using S = Stage<kFp4>;
+  using Smem = DecodeSmem<kFp4, kNT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  DecodeSmem* sm = reinterpret_cast<DecodeSmem*>(ring + p.stages * S::kBytes);
+  Smem* sm = reinterpret_cast<Smem*>(ring + p.stages * S::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&sm->full[i], kFp4 ? 1 + 32 : 1);
-      mbar_init(&sm->empty[i], 8);
-    }
+  if (tid < p.stages) {
+    mbar_init(&sm->full[tid], kFp4 ? 1 + 32 : 1);
+    mbar_init(&sm->empty[tid], 8);
+    fence_barrier_init();
+  }
+  if (tid == kConsumers) {
     mbar_init(&sm->routed, 1);
     sm->abort = 0;
-    sm->act_e[0] = p.E;
+    sm->up_done = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_w1);
     tma_prefetch_desc(&map_w3);
     tma_prefetch_desc(&map_w2);
   }
+  for (int i = tid; i < kMaxE; i += kDecThreads) {
+    sm->mask[i] = 0u;
+    if (i < kMaxS) sm->sel_e[i] = 0;
+    if (i < p.T) {
+      sm->tok_of_row[i] = i;
+      sm->row_w[i] = 1.f;
+    }
+  }
+  if (tid == 0) {
+    sm->act_e[0] = p.E;
+    sm->act_off[0] = 0;
+    sm->act_n[0] = p.T;
+  }
   __syncthreads();
 
+  // Every wait below is bounded; after one has run out the threads go on over whatever lies in shared
+  // memory (all indices stay in range), so that they keep meeting at the same barriers.
+  volatile int* abort = &sm->abort;
+  const int G = (int)gridDim.x;
   if (warp == kConsumerWarps) {
     if (kFp4 || lane == 0) produce<kFp4>(p, &map_w1, &map_w3, &map_w2, sm, ring, lane);
-    __syncwarp();   // lanes without work wait here, not at the CTA's barrier
+  } else if (warp > kConsumerWarps) {
+    route<kFp4>(p, sm, warp - kConsumerWarps - 1, lane);
   } else {
-    volatile int* abort = &sm->abort;
-    const int G = (int)gridDim.x;
-    // Every wait below is bounded; after one has run out the threads go on over whatever lies in shared
-    // memory (all indices stay in range), so that they keep meeting at the same barriers.
-    // ---------------- phase 1 and 2: routing ----------------
-    float* red0 = sm->red[0];
-    if (p.T == 1)
-      gate_partials<1>(p, 0, red0, warp, lane);
-    else
-      for (int t0 = 0; t0 < p.T; t0 += 4) gate_partials<4>(p, t0, red0, warp, lane);
-    __threadfence();
+    gate_partials<kNT>(p, sm->red[0], warp, lane);
+    if (kFp4) scale_tokens(p, tid);
     consumer_sync();
     if (tid == 0) {
       red_release_add(&p.ew->decode_arrive[0], 1);
-      grid_wait(&p.ew->decode_arrive[0], G, abort, p.ew, 404);
+      if (kFp4) grid_wait(&p.ew->decode_arrive[0], G, abort, p.ew, 408);
     }
-    consumer_sync();
-    if (warp < p.T) {
-      if (p.E <= 256) select_experts<8>(p, sm, red0 + warp * 512, warp, lane);
-      else select_experts<16>(p, sm, red0 + warp * 512, warp, lane);
-    }
-    consumer_sync();
-    build_lists(p, sm, tid);
-    consumer_sync();
-    if (tid == 0) mbar_arrive(&sm->routed);
-    if (blockIdx.x == 0) {
-      const int n = p.T * p.k;
-      if (tid < n && p.weights_out != nullptr) p.weights_out[tid] = sm->sel_w[tid];
-      if (tid < n && p.indices_out != nullptr) p.indices_out[tid] = sm->sel_e[tid];
-      if (p.counts_out != nullptr && tid < p.E) {
-        int c = 0;
-        for (int s = 0; s < n; ++s) c += sm->sel_e[s] == tid;
-        p.counts_out[tid] = c;
-      }
-    }
+    if (kFp4) consumer_sync();   // x16 is written
 
-    // ---------------- phase 3 and 4: up and down projections ----------------
-    int count = 0, buf = 0;      // stages of the tiles so far (the groups take turns)
+    int count = 0, buf = 0, tiles_up = 0;   // stages of the tiles so far (the groups take turns)
     RingPos pos;                 // and where the next one lies
+    bool routed = false;
     const uint32_t ring_addr = smem_u32(ring);
     const int grp = warp >> 3, w8 = warp & 7, g = lane >> 2, t = lane & 3;
-    const int part = S::kChunk / 8;          // elements of a stage that this warp takes
-    auto run_phase = [&](auto down_tag) {
+    const int nb1 = p.I / S::kUp, nb2 = p.d / S::kRows;
+    auto run_phase = [&](auto down_tag, TileIter it) {
       constexpr bool kDown = decltype(down_tag)::value;
-      const int K = kDown ? p.I : p.d, nb = kDown ? p.d / 16 : p.I / 8, na = sm->n_act;
-      const int ns = (K + S::kChunk - 1) / S::kChunk;
-      // the warp's next stage, whose token fragments are loaded ahead: tile, stage in it, stages before it
-      TileIter ahead(nb);
-      int ahead_s = (grp ^ count) & 1, ahead_count = count;
-      const __nv_bfloat16* rows[kNT] = {};
-      TokenFrags<kFp4, kNT> cur, nxt;
-      auto rows_of = [&](int a) {
-        const int n = sm->act_n[a], r0 = sm->act_off[a];
-        auto row = [&](int c) -> const __nv_bfloat16* {
-          if (c >= n) return nullptr;
-          return kDown ? p.h + (size_t)(r0 + c) * p.I : p.x + (size_t)sm->tok_of_row[r0 + c] * p.d;
-        };
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) rows[nt] = row(g + 8 * nt);
-      };
-      auto fetch = [&](bool first) {
-        bool moved = first;
-        while (ahead_s >= ns) {          // past the tile's end: the warp's first stage of the next one
-          ahead_count += ns;
-          ahead.next();
-          ahead_s = (grp ^ ahead_count) & 1;
-          moved = true;
+      const int K = kDown ? p.I : p.d, ns = (K + S::kChunk - 1) / S::kChunk;
+      const uint16_t* rows[kNT];               // the tile's token rows, bf16 or (MXFP4) f16, at this warp's part
+      const float* scales[kFp4 ? kNT : 1][2];
+      TokenFrags<kFp4, kNT> nxt;
+      int ready_a = -1;
+      bool all_ready = !kDown;
+      // Whether the iterator stands on a tile (waits for the lists at the first routed one).
+      auto live = [&]() {
+        if (it.a > 0 && !routed) {
+          stage_wait(&sm->routed, 0, abort, p.ew, 409);
+          routed = true;
         }
-        if (ahead.a >= na) return;
-        if (moved) rows_of(ahead.a);
-        nxt.template load<kDown>(rows, ahead_s * S::kChunk + w8 * part, K, t);
-        ahead_s += 2;
+        return it.a == 0 || it.a < sm->n_act;
       };
-      fetch(true);
-      for (TileIter it(nb); it.a < na; it.next()) {
-        const int n = sm->act_n[it.a], r0 = sm->act_off[it.a];
-        float acc[kNT][4] = {};
-        RingPos mine = pos;
-        if ((grp ^ count) & 1) mine.step(1, p.stages);
-        for (int s = (grp ^ count) & 1; s < ns; s += 2, mine.step(2, p.stages)) {
-          cur = nxt;
-          fetch(false);
-          const int slot = mine.slot;
-          if (!*abort) mbar_wait(&sm->full[slot], mine.phase, abort, p.ew, kDown ? 406 : 405);
-          __syncwarp();
-          if (s * S::kChunk + w8 * part < K) {
-            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(ring_addr + slot * S::kBytes, w8, lane, cur, acc, p.ew);
-            else consume_stage<kFp4, kDown, kNT>(ring_addr + slot * S::kBytes, w8, lane, cur, acc, p.ew);
+      auto enter = [&]() {
+        if (!all_ready && it.a != ready_a) {   // all of this expert's h is written?
+          int done = 0;
+          if (lane == 0) {
+            done = ld_acquire(&p.ew->decode_arrive[1]) >= sm->n_act * nb1;
+            if (!done) grid_wait(&p.ew->decode_ready[it.a], nb1, abort, p.ew, 402);
           }
+          all_ready = __shfl_sync(0xffffffffu, done, 0) != 0;
+          ready_a = it.a;
+        }
+        const int n = sm->act_n[it.a], r0 = sm->act_off[it.a];
+        const uint16_t* base = kDown ? p.h : kFp4 ? p.x16 : reinterpret_cast<const uint16_t*>(p.x);
+        auto place = [&](int c) { return kDown ? r0 + c : sm->tok_of_row[r0 + c]; };
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          rows[nt] = g + 8 * nt < n ? base + (size_t)place(g + 8 * nt) * K + w8 * 64 + t * 8 : nullptr;
+          if constexpr (kFp4) {
+            const float* sbase = kDown ? p.h_scale : p.x_scale;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int col = 2 * t + c + 8 * nt;
+              scales[nt][c] = col < n ? sbase + (size_t)place(col) * (K / 32) + w8 * 2 : nullptr;
+            }
+          }
+        }
+      };
+      auto fetch = [&](int s) {   // the fragments of stage s of the tile entered (zeros past its end)
+        const bool in = s * S::kChunk + w8 * 64 < K;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          nxt.v[nt][0] = nxt.v[nt][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (in && rows[nt] != nullptr) {
+            const uint4* at = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)   // written during this kernel, except x itself: read from L2
+              nxt.v[nt][kb] = kDown || kFp4 ? __ldcg(at + kb * 4) : __ldg(at + kb * 4);
+          }
+          if constexpr (kFp4) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              nxt.scale[nt][c] = in && scales[nt][c] != nullptr
+                                     ? __ldcg(reinterpret_cast<const float2*>(scales[nt][c] + s * (S::kChunk / 32)))
+                                     : make_float2(0.f, 0.f);
+          }
+        }
+      };
+      // the next stage's fragments are loaded before this one's products where the registers hold both
+      // (bf16 with one column tile: 3 % faster), behind them elsewhere (no spills: 6 % faster)
+      constexpr bool kEarly = !kFp4 && kNT == 1;
+      bool more = live();
+      if (more) {
+        enter();
+        fetch((grp ^ count) & 1);
+      }
+      while (more) {
+        const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
+        float acc[S::kRowTiles][kNT][4] = {};
+        RingPos mine = pos;
+        int s = (grp ^ count) & 1;
+        if (s) mine.step(1, p.stages);
+        for (; s < ns; s += 2, mine.step(2, p.stages)) {
+          const TokenFrags<kFp4, kNT> cur = nxt;
+          if (kEarly && s + 2 < ns) fetch(s + 2);
+          stage_wait(&sm->full[mine.slot], mine.phase, abort, p.ew, kDown ? 406 : 405);
+          if (kFp4 || s * S::kChunk + w8 * 64 < K) {
+            const uint32_t stage = ring_addr + mine.slot * S::kBytes;
+            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(stage, w8, lane, cur, acc, p.ew);
+            else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, cur, acc, p.ew);
+          }
+          if (!kEarly && s + 2 < ns) fetch(s + 2);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->empty[slot]);
+          if (lane == 0) mbar_arrive(&sm->empty[mine.slot]);
         }
         count += ns;
         pos.step(ns, p.stages);
+        // the next tile's first fragments are under way while this one is added up
+        it.next();
+        more = live();
+        if (more) {
+          enter();
+          fetch((grp ^ count) & 1);
+        }
         float* red = sm->red[buf];
-        buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
-        put_partials(red, warp, lane, acc, n <= 8 ? 1 : 2);
+        if (S::kRedBufs == 2) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
+        put_partials<kFp4, kNT>(red, warp, lane, acc, n <= 8 ? 1 : 2);
         consumer_sync();
-        if (kDown) {
-          const int c = tid >> 4, r = tid & 15;
-          if (c < n) p.out[(size_t)(r0 + c) * p.d + it.blk * 16 + r] = sum_partials(red, c, r);
+        if constexpr (kDown) {
+          for (int i = tid; i < n * S::kRows; i += kConsumers) {
+            const int c = i / S::kRows, r = i % S::kRows;
+            p.out[(size_t)(r0 + c) * p.d + blk * S::kRows + r] = sum_partials<kFp4, kNT>(red, c, r);
+          }
+          if (S::kRedBufs == 1) consumer_sync();
         } else {
-          const int c = tid >> 3, f = tid & 7;
-          if (c < n) {
-            const float gate = sum_partials(red, c, f), val = sum_partials(red, c, f + 8);
-            const float w = p.weight_in_expert && it.a > 0 ? sm->row_w[r0 + c] : 1.f;
-            const int at = kFp4 ? (f < 4 ? 2 * f : 2 * f - 7) : f;   // MXFP4: the octet's order 0 4 1 5 2 6 3 7
-            p.h[(size_t)(r0 + c) * p.I + it.blk * 8 + at] = __float2bfloat16_rn(swiglu(gate, val, p.swiglu_limit, w));
+          // feature f of token c: gate and value sums, eight rows apart in their row tile
+          const int c = tid / S::kUp, f = tid % S::kUp;
+          const bool in = c < n;
+          float h = 0.f;
+          if (in) {
+            const int r = (f >> 3) * 16 + (f & 7);
+            const float w = p.weight_in_expert && a > 0 ? sm->row_w[r0 + c] : 1.f;
+            h = swiglu(sum_partials<kFp4, kNT>(red, c, r), sum_partials<kFp4, kNT>(red, c, r + 8), p.swiglu_limit, w);
+          }
+          if constexpr (kFp4) {   // a warp holds one token's block of 32: its scale, then f16
+            const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu) >> 23);
+            if (in) {
+              const __half v = __float2half_rn(h * block_up(eb));
+              p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
+              if (lane == 0) p.h_scale[(size_t)(r0 + c) * (p.I / 32) + blk] = block_down(eb);
+            }
+            consumer_sync();
+            if (tid == 0) {
+              __threadfence_block();
+              *(volatile int*)&sm->up_done = ++tiles_up;
+            }
+          } else {
+            if (in) {
+              const __nv_bfloat16 v = __float2bfloat16_rn(h);
+              p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
+            }
+            if (warp < 4) writers_sync();   // 16 tokens x 8 features: the first 128 threads wrote
+            if (tid == 0) {
+              __threadfence_block();
+              *(volatile int*)&sm->up_done = ++tiles_up;
+            }
           }
         }
       }
     };
-    // all CTAs past a phase before the next reads its rows
-    auto grid_barrier = [&](int which, int site) {
-      __threadfence();
-      consumer_sync();
-      if (tid == 0) {
-        red_release_add(&p.ew->decode_arrive[which], 1);
-        grid_wait(&p.ew->decode_arrive[which], G, abort, p.ew, site);
-      }
-      consumer_sync();
-    };
-    run_phase(std::false_type{});
-    grid_barrier(1, 402);
-    run_phase(std::true_type{});
-    grid_barrier(2, 407);
+    run_phase(std::false_type{}, TileIter(nb1));
+    run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2));
+    consumer_sync();
+    if (tid == 0) {
+      red_release_add(&p.ew->decode_arrive[2], 1);
+      grid_wait(&p.ew->decode_arrive[2], G, abort, p.ew, 407);
+    }
+    consumer_sync();
 
-    // ---------------- phase 5: combine, slot order then the shared expert ----------------
+    // ---------------- combine, slot order then the shared expert ----------------
     const int d4 = p.d / 4;
     for (int i = blockIdx.x * kConsumers + tid; i < p.T * d4; i += G * kConsumers) {
       const int t = i / d4, f = (i - t * d4) * 4;
@@ -839,37 +1084,40 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // the last CTA to get here leaves the grid's counters at zero (nobody waits on them any more)
   __syncwarp();
   __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    if (atomicAdd(&p.ew->decode_done, 1) == (int)gridDim.x - 1) {
-      p.ew->decode_arrive[0] = p.ew->decode_arrive[1] = p.ew->decode_arrive[2] = 0;
-      p.ew->decode_done = 0;
-    }
+  if (tid == 0) sm->last = atomicAdd(&p.ew->decode_done, 1) == G - 1;
+  __syncthreads();
+  if (sm->last) {
+    if (tid < kMaxAct) p.ew->decode_ready[tid] = 0;
+    if (tid < 4) p.ew->decode_arrive[tid] = 0;
+    if (tid == 4) p.ew->decode_done = 0;
   }
 }
 
 }  // namespace
 
 int decode_gate_splits(int E, int d) {
-  // about one unit of 16 router rows per SM of a B200, at least 128 elements of k each
-  return std::max(1, std::min(d / 128, 148 / (E / kGateRows)));
+  // at most one unit of 16 router rows per SM of a B200, at least 128 elements of k each, and no more slices
+  // than the selection reads at once
+  return std::max(1, std::min({d / 128, 148 / (E / kGateRows), 8}));
 }
 
 cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
                                 bool fp4, int num_sms, cudaStream_t stream) {
   const size_t smem = 227 * 1024;
   const size_t stage = fp4 ? Stage<true>::kBytes : Stage<false>::kBytes;
+  const size_t fixed = fp4 ? (p.T <= 8 ? sizeof(DecodeSmem<true, 1>) : sizeof(DecodeSmem<true, 2>))
+                           : (p.T <= 8 ? sizeof(DecodeSmem<false, 1>) : sizeof(DecodeSmem<false, 2>));
   // An even number: a slot then always belongs to the same group of consumer warps, which waits for each of
   // its fills in turn.  With an odd one the groups would share a slot, and the group of its second fill,
   // running ahead inside a long tile, would take a first fill that has not landed for its own (a barrier's
   // parity tells two successive phases apart, not three).
-  p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - sizeof(DecodeSmem)) / stage) & ~1;
+  p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - fixed) / stage) & ~1;
   auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1> : layer_decode_kernel<true, 2>)
                     : (p.T <= 8 ? layer_decode_kernel<false, 1> : layer_decode_kernel<false, 2>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // no more CTAs than any phase has work for: small layers pay for each arrival at the barriers
-  const long tiles = (long)(std::min(p.T * p.k, p.E) + 1) * std::max(p.I / 8, p.d / 16);
+  const long tiles = (long)(std::min(p.T * p.k, p.E) + 1) * std::max(p.I / (fp4 ? 32 : 8), p.d / (fp4 ? 64 : 16));
   const int units = p.E / kGateRows * p.gate_splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long>(num_sms, std::max<long>(tiles, units)));

@@ -164,7 +164,12 @@ struct DecodeParams {
   const uint8_t *w1, *w3, *w2;     // bf16 rows, or packed E2M1 codes
   const uint8_t *w1s, *w3s, *w2s;  // UE8M0 block scales (MXFP4), else null
   float* partial;             // [gate_splits, T, E] scratch
-  __nv_bfloat16* h;           // [T + T * k, I] scratch: shared rows first, then the active experts'
+  uint16_t* x16;              // MXFP4: [T, d] scratch, x in f16 blocks of 32, and
+  float* x_scale;             //   their scales [T, d / 32]
+  uint16_t* h;                // [T + T * k, I] scratch (bf16; MXFP4: f16 blocks): shared rows first, then the experts'
+  float* h_scale;             // MXFP4: [T + T * k, I / 32] scratch
+  int32_t* route_e;           // [T * k] scratch: the selection, handed round the grid
+  float* route_w;             // [T * k]
   float* out;                 // [T + T * k, d] scratch
   __nv_bfloat16* y;           // [T, d]
   float* weights_out;         // [T, k] or null
@@ -174,7 +179,7 @@ struct DecodeParams {
 };
 int decode_gate_splits(int E, int d);
 // w1 / w3 / w2: the stacked expert matrices as [128 bytes, rows, bytes of a row / 128] in boxes of
-// 128 bytes x 8 rows x 8 (bf16) or 4 (packed codes), 128-byte swizzle.
+// 128 bytes x 8 rows x 8 (bf16) or 128 bytes x 32 rows x 2 (packed codes), 128-byte swizzle.
 cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
                                 bool fp4, int num_sms, cudaStream_t stream);
 

@@ -81,7 +81,7 @@ namespace {
 // first, the scales 1 KiB-aligned after them) and the quantised x in a region of its own.
 struct WsLayout {
   size_t err, flag, planes, indices, weights, counts, offsets, row_of_slot, tok_of_row, w_perm, hist, base,
-      chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, total;
+      chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, dec_x16, dec_x_scale, dec_h_scale, total;
   size_t xp_scales, h_scales, xq_scales;   // offsets of the scales inside x_perm, h and xq
 };
 
@@ -123,6 +123,9 @@ WsLayout ws_layout(const moe_layer_desc& d, int T) {
   const bool dec = T <= MOE_DECODE_MAX_TOKENS;
   L.dec_partial = take(dec ? (size_t)moe::decode_gate_splits(d.n_experts, d.dim) * T * E * 4 : 0);
   L.dec_out = take(dec ? (S + T) * D * 4 : 0);
+  L.dec_x16 = take(dec ? (size_t)T * D * 2 : 0);
+  L.dec_x_scale = take(dec ? (size_t)T * (D / 32) * 4 : 0);
+  L.dec_h_scale = take(dec ? (S + T) * (I / 32) * 4 : 0);
   L.total = o;
   return L;
 }
@@ -882,17 +885,22 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
     p.w1 = bytes(w1); p.w3 = bytes(w3); p.w2 = bytes(w2);
   }
   p.partial = at<float>(ws, L.dec_partial);
-  p.h = at<__nv_bfloat16>(ws, L.h);
+  p.route_e = at<int32_t>(ws, L.indices);
+  p.route_w = at<float>(ws, L.weights);
+  p.x16 = at<uint16_t>(ws, L.dec_x16);
+  p.x_scale = at<float>(ws, L.dec_x_scale);
+  p.h = at<uint16_t>(ws, L.h);
+  p.h_scale = at<float>(ws, L.dec_h_scale);
   p.out = at<float>(ws, L.dec_out);
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.weights_out = weights_out; p.indices_out = indices_out; p.counts_out = counts_out;
   p.ew = at<ErrorWord>(ws, L.err);
   CUtensorMap m1, m3, m2;
   const uint64_t n = d.n_experts + 1, per = fp4 != nullptr ? 1 : 4;   // bytes of two weights
-  const uint32_t cols = fp4 != nullptr ? 4 : 8;
-  if (!make_map_columns(&m1, p.w1, n * d.inter_dim, d.dim / 2 * per, 8, cols) ||
-      !make_map_columns(&m3, p.w3, n * d.inter_dim, d.dim / 2 * per, 8, cols) ||
-      !make_map_columns(&m2, p.w2, n * d.dim, d.inter_dim / 2 * per, 8, cols))
+  const uint32_t rows = fp4 != nullptr ? 32 : 8, cols = fp4 != nullptr ? 2 : 8;
+  if (!make_map_columns(&m1, p.w1, n * d.inter_dim, d.dim / 2 * per, rows, cols) ||
+      !make_map_columns(&m3, p.w3, n * d.inter_dim, d.dim / 2 * per, rows, cols) ||
+      !make_map_columns(&m2, p.w2, n * d.dim, d.inter_dim / 2 * per, rows, cols))
     return MOE_ERR_CUDA;
   return cuda_status(moe::launch_layer_decode(m1, m3, m2, p, fp4 != nullptr, num_sms(), s));
 }

@@ -384,38 +384,49 @@ def moe_forward_mxfp4(desc, x, w_gate, w, y, ws: Workspace, bias=None, logit_off
                                  _stream(stream)), "moe_forward_mxfp4")
 
 
-def _shape(t: Optional[torch.Tensor], dtype, shape, name: str):
+def _shape(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     """The checks of the few-token layer and the linear projection: type, exact shape, current device."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == device):
         return
     _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out):
+def _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
+                   dev):
     T, d, E, k = x.shape[0], desc.dim, desc.n_experts, desc.topk
-    _shape(x, torch.bfloat16, (T, d), "x"); _shape(y, torch.bfloat16, (T, d), "y")
-    _shape(w_gate, torch.float32, (E, d), "w_gate")
-    _shape(bias, torch.float32, (E,), "bias"); _shape(logit_offset, torch.float32, (E,), "logit_offset")
-    _shape(token_ids, torch.int32, (T,), "token_ids")
+    f32, i32 = torch.float32, torch.int32
+    _shape(x, torch.bfloat16, (T, d), "x", dev)
+    _shape(y, torch.bfloat16, (T, d), "y", dev)
+    _shape(w_gate, f32, (E, d), "w_gate", dev)
+    _shape(bias, f32, (E,), "bias", dev)
+    _shape(logit_offset, f32, (E,), "logit_offset", dev)
+    if token_ids is not None:
+        _shape(token_ids, i32, (T,), "token_ids", dev)
     if tid2eid is not None:
-        _shape(tid2eid, torch.int32, (tid2eid.shape[0], k), "tid2eid")
-    _shape(weights_out, torch.float32, (T, k), "weights_out"); _shape(indices_out, torch.int32, (T, k), "indices_out")
-    _shape(counts_out, torch.int32, (E,), "counts_out")
+        _shape(tid2eid, i32, (tid2eid.shape[0], k), "tid2eid", dev)
+    if weights_out is not None:
+        _shape(weights_out, f32, (T, k), "weights_out", dev)
+    if indices_out is not None:
+        _shape(indices_out, i32, (T, k), "indices_out", dev)
+    _shape(counts_out, i32, (E,), "counts_out", dev)
+    return T
 
 
 def moe_decode(desc, x, w_gate, w1, w3, w2, y, ws: Workspace, bias=None, logit_offset=None, token_ids=None,
                tid2eid=None, weights_out=None, indices_out=None, counts_out=None, stream=None):
     """moe_forward for at most MOE_DECODE_MAX_TOKENS tokens in one kernel launch."""
-    _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out)
+    dev = torch.cuda.current_device()
+    T = _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
+                       dev)
     E1, d, I = desc.n_experts + 1, desc.dim, desc.inter_dim
-    _shape(w1, torch.bfloat16, (E1, I, d), "w1"); _shape(w3, torch.bfloat16, (E1, I, d), "w3")
-    _shape(w2, torch.bfloat16, (E1, d, I), "w2")
+    _shape(w1, torch.bfloat16, (E1, I, d), "w1", dev)
+    _shape(w3, torch.bfloat16, (E1, I, d), "w3", dev)
+    _shape(w2, torch.bfloat16, (E1, d, I), "w2", dev)
     vocab = 0 if tid2eid is None else tid2eid.shape[0]
-    _check(lib.moe_decode(ctypes.byref(desc), x.shape[0], _ptr(x), _ptr(token_ids), _ptr(tid2eid), vocab,
+    _check(lib.moe_decode(ctypes.byref(desc), T, _ptr(x), _ptr(token_ids), _ptr(tid2eid), vocab,
                           _ptr(w_gate), _ptr(bias), _ptr(logit_offset), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(y),
                           _ptr(weights_out), _ptr(indices_out), _ptr(counts_out), ws.ptr, ws.nbytes,
                           _stream(stream)), "moe_decode")
@@ -424,14 +435,16 @@ def moe_decode(desc, x, w_gate, w1, w3, w2, y, ws: Workspace, bias=None, logit_o
 def moe_decode_mxfp4(desc, x, w_gate, w, y, ws: Workspace, bias=None, logit_offset=None, token_ids=None,
                      tid2eid=None, weights_out=None, indices_out=None, counts_out=None, stream=None):
     """moe_decode with MXFP4 expert weights ``w`` (see mxfp4_weights) and bf16 activations."""
-    _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out)
+    dev = torch.cuda.current_device()
+    T = _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
+                       dev)
     E1, d, I = desc.n_experts + 1, desc.dim, desc.inter_dim
     for n, rows, cols in (("w1", I, d), ("w3", I, d), ("w2", d, I)):
-        _shape(getattr(w, n), torch.uint8, (E1, rows, cols // 2), n)
-        _shape(getattr(w, n + "s"), torch.uint8, (E1, rows, cols // 32), n + "s")
+        _shape(getattr(w, n), torch.uint8, (E1, rows, cols // 2), n, dev)
+        _shape(getattr(w, n + "s"), torch.uint8, (E1, rows, cols // 32), n + "s", dev)
     vocab = 0 if tid2eid is None else tid2eid.shape[0]
     mw = mxfp4_weights(w)
-    _check(lib.moe_decode_mxfp4(ctypes.byref(desc), x.shape[0], _ptr(x), _ptr(token_ids), _ptr(tid2eid), vocab,
+    _check(lib.moe_decode_mxfp4(ctypes.byref(desc), T, _ptr(x), _ptr(token_ids), _ptr(tid2eid), vocab,
                                 _ptr(w_gate), _ptr(bias), _ptr(logit_offset), ctypes.byref(mw), _ptr(y),
                                 _ptr(weights_out), _ptr(indices_out), _ptr(counts_out), ws.ptr, ws.nbytes,
                                 _stream(stream)), "moe_decode_mxfp4")
