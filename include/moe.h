@@ -412,6 +412,45 @@ moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x
                             moe_stream_t stream);
 
 /*
+ * The linear projection around a layer: y = act(x . w^T + bias) + residual, with fp32 accumulation and one
+ * rounding, for what a decoder block has beside its experts -- projections back into the residual
+ * stream, a dense FFN's matrices, the output head over the vocabulary.  Any number of tokens from none:
+ * up to 16 run as a weight stream, more as tiles on the tensor cores.  The pages have no counterpart.
+ *   silu(z) = z / (1 + e^-z), gelu(z) = z/2 (1 + erf(z / sqrt 2)), gelu_tanh its form with
+ *   tanh(sqrt(2/pi) (z + 0.044715 z^3)).
+ * x: T rows of K = in_features bf16, row t at x + t * ldx; w [N, K] bf16 contiguous, N = out_features;
+ * bias [N] fp32 or NULL; residual: T rows of N bf16 at stride ldr, or NULL (ldr is then not read);
+ * y (out): T rows of N bf16, or fp32 when out_fp32 is 1, at stride ldy.  Strides are in elements.
+ * y may be the residual itself (bf16, the same pointer and stride); it must not overlap x, w or bias.
+ * What lies between the rows of y (ldy > N) is left as it was.
+ * Needs K % 8 == 0 and ldx % 8 == 0 (MOE_ERR_UNSUPPORTED otherwise); x and w 16-byte aligned, the others
+ * aligned to their elements, ldx >= K, ldy >= N, ldr >= N (MOE_ERR_INVALID otherwise).
+ * ws: moe_linear_workspace_bytes(desc, T) bytes, 1 KiB aligned, cleared once by moe_workspace_init; a
+ * workspace serves one call at a time, and any descriptor it is large enough for.  Results do not depend
+ * on scheduling.
+ */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_activation;
+
+typedef struct {
+  int in_features;            /* K */
+  int out_features;           /* N */
+  moe_activation activation;
+  int out_fp32;               /* 0: y is bf16; 1: y is fp32 */
+} moe_linear_desc;
+
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc, int T);
+
+moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int64_t ldx, const moe_bf16* w,
+                      const float* bias, const moe_bf16* residual, int64_t ldr, void* y, int64_t ldy, void* ws,
+                      size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns the first error a kernel recorded in `ws` since the last
  * call (MOE_OK if none) and clears it.  *info (host, may be NULL) receives the offending value.
  */

@@ -19,7 +19,7 @@
 namespace moe {
 
 // ------------------------------------------------------------------------------------------------
-// control words (first 1024 bytes of every workspace)
+// control words (first 4096 bytes of every workspace)
 // ------------------------------------------------------------------------------------------------
 struct ErrorWord {
   int status;           // 0 or the first moe_status recorded
@@ -28,7 +28,8 @@ struct ErrorWord {
   int decode_arrive[4]; // the one-launch layer's grid counters: logits, up tiles, down, tokens (0 between calls)
   int decode_done;      //   and CTAs finished
   int decode_ready[144];  // its up tiles finished, per active expert (0 between calls)
-  int pad[104];
+  int linear_done[512];   // the linear projection's parts of a tile finished (0 between calls)
+  int pad[360];
 };
 
 __device__ __forceinline__ void record_error(ErrorWord* ew, int status, int info) {

@@ -183,6 +183,35 @@ int decode_gate_splits(int E, int d);
 cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, const CUtensorMap& w2, DecodeParams p,
                                 bool fp4, int num_sms, cudaStream_t stream);
 
+// The linear projection (linear.cu).
+constexpr int kLinearStreamTokens = 16;   // batches up to this run as a weight stream
+struct LinearParams {
+  int T, K, N;
+  int act, out_fp32;
+  int y_vec, residual_vec;    // rows of y / residual start on 16-byte boundaries
+  int stages;                 // set by the launcher
+  int m_tiles, n_tiles, splits;
+  int test_stall;
+  long long ldx, ldy, ldr;    // elements
+  const __nv_bfloat16* x;
+  const float* bias;          // [N] or null
+  const __nv_bfloat16* residual;  // or null
+  void* y;
+  float* scratch;
+  ErrorWord* ew;
+};
+// How a projection of T tokens runs: as a weight stream, or in tiles of single CTAs or CTA pairs with K cut
+// into `splits`.  w_box: weight rows per box of its tensor map (64 elements of k wide).
+struct LinearPlan {
+  enum Kind { kStream, kSolo, kPair } kind;
+  int m_tiles, n_tiles, splits;
+  int w_box;
+  size_t scratch_floats;
+};
+LinearPlan linear_plan(int T, int K, int N, int num_sms);
+cudaError_t launch_linear(const LinearPlan& plan, const CUtensorMap& map_x, const CUtensorMap& map_w, LinearParams p,
+                          int num_sms, cudaStream_t stream);
+
 // Host-side launchers, one per kernel; each returns the launch's cudaError_t.
 cudaError_t launch_gate_planes(const float* w, __nv_bfloat16* planes, long n, int* inexact_flag, int num_sms,
                                cudaStream_t stream);

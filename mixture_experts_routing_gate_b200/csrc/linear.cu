@@ -1,0 +1,704 @@
+// The linear projection with its epilogue: y = act(x . w^T + bias) + residual, x [T, K] and w [N, K] bf16,
+// fp32 accumulation, y bf16 or fp32.
+//
+// Two kernels.  Up to 16 tokens the weights are read for at most sixteen columns of products, so what counts
+// is the weight stream (linear_stream_kernel, mma.sync); above, the products are tiles on the tcgen05 tensor
+// cores (linear_gemm_kernel).  Both add the bias, apply the activation and add the residual to the fp32
+// accumulators, which are rounded once.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+// ------------------------------------------------------------------------------------------------
+// the epilogue
+// ------------------------------------------------------------------------------------------------
+// NaN goes through every branch.  silu and the tanh form of gelu are z / (1 + e^-a) (no cancellation for
+// negative z); the exact gelu uses erfc for the same reason.
+__device__ __forceinline__ float activate(float z, int act) {
+  if (act == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
+  if (act == MOE_ACT_SILU) return __fdiv_rn(z, 1.f + __expf(-z));
+  if (act == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+  if (act == MOE_ACT_GELU_TANH) return __fdiv_rn(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+  return z;
+}
+
+// Eight consecutive outputs (columns c .. c + 7 of row t) from their accumulators.
+__device__ __forceinline__ void finish8(const LinearParams& p, int t, long c, const float (&z)[8], const float (&bias)[8]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate(z[i] + bias[i], p.act);
+  const bool whole = c + 8 <= p.N;
+  if (p.residual != nullptr) {
+    const __nv_bfloat16* r = p.residual + (size_t)t * p.ldr + c;
+    if (whole && p.residual_vec) {
+      const uint4 q = *reinterpret_cast<const uint4*>(r);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.N) v[i] += __bfloat162float(r[i]);
+    }
+  }
+  if (p.out_fp32) {
+    float* y = static_cast<float*>(p.y) + (size_t)t * p.ldy + c;
+    if (whole && p.y_vec) {
+      reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.N) y[i] = v[i];
+    }
+  } else {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (size_t)t * p.ldy + c;
+    if (whole && p.y_vec) {
+      *reinterpret_cast<uint4*>(y) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
+                                                bf16x2_bits(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.N) y[i] = __float2bfloat16_rn(v[i]);
+    }
+  }
+}
+
+__device__ __forceinline__ void load_bias8(const LinearParams& p, long c, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = p.bias != nullptr && c + i < p.N ? __ldg(p.bias + c + i) : 0.f;
+}
+
+// ------------------------------------------------------------------------------------------------
+// up to 16 tokens: a weight stream
+//
+// Work is cut into stages of 64 weight rows x 128 elements of k (16 KB), numbered tile by tile, and every
+// CTA takes an equal run of them, whatever the number of tiles: 112 tiles of 64 rows on 148 SMs would keep a
+// quarter of them idle.  A tile that spans several CTAs is added up by the last of them to arrive, from
+// fp32 partials in the workspace and in the order of the CTAs, so results do not depend on scheduling
+// and no CTA waits for another.
+//
+// One thread keeps TMA copies in flight into a ring of about 180 KB, sixteen warps compute: two groups taking
+// alternate stages (the ring has an even number of slots, so a slot always belongs to one group), in each
+// group four warps along k times two along the rows.  The weights are the 16-row operand of mma.sync
+// m16n8k16, the tokens its columns; thread t of a quad holds 8 consecutive elements of k for both, so a
+// weight fragment is one conflict-free 16-byte load from TMA's 128-byte swizzle and a token fragment one
+// 16-byte load from L1 or L2, a stage ahead.
+// ------------------------------------------------------------------------------------------------
+constexpr int kStreamWarps = 16, kStreamConsumers = kStreamWarps * 32, kStreamThreads = kStreamConsumers + 32;
+constexpr int kStreamRows = 64, kStreamK = 128, kStreamBytes = kStreamRows * kStreamK * 2;
+constexpr int kStreamMaxStages = 12;
+constexpr int kStreamPitch = kStreamRows + 4;   // floats per token column of the exchange (bank = 8 t + g)
+
+template <int kNT>
+struct StreamSmem {
+  uint64_t full[kStreamMaxStages], empty[kStreamMaxStages];
+  int abort, last;
+  alignas(16) float red[8][8 * kNT][kStreamPitch];
+};
+
+__device__ __forceinline__ void stream_sync() {   // the consumer warps, whole
+  __syncwarp();
+  asm volatile("bar.sync 1, 512;" ::: "memory");
+}
+static_assert(kStreamConsumers == 512, "the named barrier's thread count");
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// First stage of CTA c of G, and the CTA that has stage u, of U stages dealt in equal runs.
+// (A stage is 16 KB of weights, so their number fits an int.)
+__device__ __forceinline__ int run_start(int U, int c, int G) { return (int)((long)U * c / G); }
+__device__ __forceinline__ int run_owner(int U, int u, int G) { return (int)((((long)u + 1) * G - 1) / U); }
+
+template <int kNT>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    linear_stream_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ LinearParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* sm = reinterpret_cast<StreamSmem<kNT>*>(ring + p.stages * kStreamBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int G = (int)gridDim.x, ns = (p.K + kStreamK - 1) / kStreamK;
+  const int U = (p.N + kStreamRows - 1) / kStreamRows * ns;
+  const int u0 = run_start(U, blockIdx.x, G), u1 = run_start(U, blockIdx.x + 1, G);
+  volatile int* abort = &sm->abort;
+  if (tid < p.stages) {
+    mbar_init(&sm->full[tid], 1);
+    mbar_init(&sm->empty[tid], 8);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    sm->abort = 0;
+    tma_prefetch_desc(&map_w);
+  }
+  __syncthreads();
+  pdl_begin();
+
+  if (warp == kStreamWarps) {
+    if (lane == 0 && !p.test_stall) {
+      int slot = 0, issued = 0;
+      uint32_t ph = 0;
+      int row = u0 / ns * kStreamRows, k = u0 % ns * kStreamK;
+      for (int u = u0; u < u1; ++u) {
+        if (!mbar_wait(&sm->empty[slot], ph ^ 1, abort, p.ew, 501)) break;
+        uint8_t* dst = ring + slot * kStreamBytes;
+        mbar_arrive_expect_tx(&sm->full[slot], kStreamBytes);   // whole boxes: zeros past K and N
+        tma_load_2d(dst, &map_w, &sm->full[slot], k, row);
+        tma_load_2d(dst + kStreamBytes / 2, &map_w, &sm->full[slot], k + 64, row);
+        ++issued;
+        if ((k += kStreamK) >= p.K) {
+          k = 0;
+          row += kStreamRows;
+        }
+        if (++slot == p.stages) {
+          slot = 0;
+          ph ^= 1;
+        }
+      }
+      if (*abort)   // let every copy already issued land before the CTA leaves
+        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+          mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+    }
+  } else {
+    const int grp = warp >> 3, wk = warp & 3, wr = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
+    const uint32_t ring_addr = smem_u32(ring);
+    uint4 nxt[kNT];
+    auto fetch = [&](int u) {   // this warp's 32 elements of k of stage u, for token columns g and g + 8
+      const int k = u % ns * kStreamK + wk * 32 + t * 8;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        nxt[nt] = g + 8 * nt < p.T && k < p.K
+                      ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(g + 8 * nt) * p.ldx + k))
+                      : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int slot = grp % p.stages;
+    uint32_t ph = 0;
+    if (u0 + grp < u1) fetch(u0 + grp);
+    for (int u = u0; u < u1;) {
+      const int tile = u / ns, end = min((tile + 1) * ns, u1);
+      const bool starts = u == tile * ns, ends = end == (tile + 1) * ns;
+      float acc[2][kNT][4] = {};
+      for (int s = u + ((u - u0 + grp) & 1); s < end; s += 2) {   // the group's stages: those of its parity from u0
+        uint4 cur[kNT];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) cur[nt] = nxt[nt];
+        if (s + 2 < u1) fetch(s + 2);
+        if (!mbar_try_wait(&sm->full[slot], ph) && !*abort) mbar_wait(&sm->full[slot], ph, abort, p.ew, 502);
+        __syncwarp();
+        // elements [32 wk, 32 wk + 32) are half of 64-element column wk / 2
+        const uint32_t at = ring_addr + slot * kStreamBytes + (wk >> 1) * (kStreamBytes / 2) +
+                            (wr * 32 + g) * 128 + ((((wk & 1) * 4 + t) ^ g) << 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 lo = lds128(at + i * 16 * 128), hi = lds128(at + (i * 16 + 8) * 128);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            mma_16816(acc[i][nt], lo.x, hi.x, lo.y, hi.y, cur[nt].x, cur[nt].y);
+            mma_16816(acc[i][nt], lo.z, hi.z, lo.w, hi.w, cur[nt].z, cur[nt].w);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->empty[slot]);
+        slot += 2;
+        if (slot >= p.stages) {
+          slot -= p.stages;
+          ph ^= 1;
+        }
+      }
+      stream_sync();   // the exchange buffer is free
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          float* c = &sm->red[grp * 4 + wk][nt * 8 + 2 * t][wr * 32 + i * 16 + g];
+          c[0] = acc[i][nt][0];
+          c[kStreamPitch] = acc[i][nt][1];
+          c[8] = acc[i][nt][2];
+          c[kStreamPitch + 8] = acc[i][nt][3];
+        }
+      stream_sync();
+      // thread: eight rows of one token's column
+      const int col = tid >> 3, r8 = (tid & 7) * 8;
+      const bool in = col < p.T;
+      const long c8 = (long)tile * kStreamRows + r8;
+      float z[8] = {};
+      if (in) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float4* src = reinterpret_cast<const float4*>(&sm->red[w][col][r8]);
+          const float4 a = src[0], b = src[1];
+          z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+          z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+        }
+      }
+      bool finish = in;
+      if (!(starts && ends)) {
+        // a slot per CTA for the tile it continues and one for the tile it leaves unfinished
+        const int c0 = run_owner(U, tile * ns, G), c1 = run_owner(U, (tile + 1) * ns - 1, G);
+        constexpr int kSlot = kStreamRows * 16;
+        auto place = [&](int c) { return p.scratch + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kSlot + col * kStreamRows + r8; };
+        if (in) {
+          float4* dst = reinterpret_cast<float4*>(place(blockIdx.x));
+          dst[0] = make_float4(z[0], z[1], z[2], z[3]);
+          dst[1] = make_float4(z[4], z[5], z[6], z[7]);
+          __threadfence();
+        }
+        stream_sync();
+        if (tid == 0) {
+          const int last = atomicAdd(&p.ew->linear_done[c0], 1) == c1 - c0;
+          if (last) p.ew->linear_done[c0] = 0;
+          __threadfence();
+          sm->last = last;
+        }
+        stream_sync();
+        finish = in && sm->last;
+        if (finish) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const float4* src = reinterpret_cast<const float4*>(place(c));
+            const float4 a = __ldcg(src), b = __ldcg(src + 1);
+            z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+            z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+          }
+        }
+      }
+      if (finish && c8 < p.N) {
+        float b[8];
+        load_bias8(p, c8, b);
+        finish8(p, col, c8, z, b);
+      }
+      u = end;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------------------------------------
+// more tokens: tiles on the tcgen05 tensor cores
+//
+// A CTA's tile is 128 tokens (the MMA's M, a TMEM lane each) by kBN features (its N).  kPair: clusters of two
+// CTAs share MMAs of M = 256 by kBN = 256 (cta_group::2): each loads its 128 tokens and half of the weight
+// rows, 32 KB for 64 elements of k, half of what two single CTAs load for the same products.  Persistent and
+// warp-specialised: warp 0 TMA, warp 1 MMA (even CTA), eight epilogue warps, two accumulators in TMEM so that
+// a tile's epilogue runs beside the next tile's MMAs.  The epilogue brings 32 x 32 blocks through shared
+// memory (pitch 33: both directions free of bank conflicts) so that a lane finishes eight consecutive
+// features of a row and stores 16 bytes.
+//
+// splits > 1 (fewer tiles than SMs): K is cut, each unit leaves fp32 partials in the workspace and the last
+// CTA of a tile to arrive adds them in order and finishes; nobody waits.
+// ------------------------------------------------------------------------------------------------
+constexpr int kGemmStagesMax = 8;
+constexpr int kEpiWarps = 8;
+constexpr int kLinThreads = 64 + kEpiWarps * 32;
+constexpr int kEpiPitch = 33;
+
+struct LinGemmSmem {
+  uint64_t full[kGemmStagesMax], empty[kGemmStagesMax];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort, last;
+  float stage[kEpiWarps][32 * kEpiPitch];
+};
+
+template <bool kPair>
+struct LinTile {
+  static constexpr int kBN = kPair ? 256 : 128;
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = kBN / kCtas * 128;
+  static constexpr int kStage = kABytes + kBBytes;
+};
+
+__device__ __forceinline__ void epilogue_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+static_assert(kEpiWarps * 32 == 256, "the named barrier's thread count");
+
+// Unit w: tile and slice of k.  Tiles run through groups of eight token blocks, all of a group's token blocks
+// for one feature block before the next, so that what runs at a time shares weights and tokens in L2.
+struct LinUnit {
+  int m, n, k0, k1, tile, split;
+};
+__device__ __forceinline__ LinUnit lin_unit(const LinearParams& p, int w) {
+  LinUnit u;
+  u.tile = w / p.splits;
+  u.split = w - u.tile * p.splits;
+  const int nk = (p.K + 63) / 64, group = 8 * p.n_tiles, gi = u.tile / group, r = u.tile - gi * group;
+  const int rows = min(8, p.m_tiles - gi * 8);
+  u.n = r / rows;
+  u.m = gi * 8 + (r - u.n * rows);
+  u.k0 = (int)((long)nk * u.split / p.splits);
+  u.k1 = (int)((long)nk * (u.split + 1) / p.splits);
+  return u;
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       const __grid_constant__ LinearParams p) {
+  using L = LinTile<kPair>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* sm = reinterpret_cast<LinGemmSmem*>(smem + p.stages * L::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int first = kPair ? blockIdx.x >> 1 : blockIdx.x, step = kPair ? gridDim.x >> 1 : gridDim.x;
+  const int units = p.m_tiles * p.n_tiles * p.splits;
+  volatile int* abort = &sm->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sm->full[s], 1);
+      mbar_init(&sm->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sm->acc_full[a], 1);
+      mbar_init(&sm->acc_empty[a], L::kCtas * kEpiWarps);
+    }
+    mbar_init(&sm->drain, 1);
+    sm->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  if (warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(&sm->tmem_base, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sm->tmem_base, 512);
+      tmem_relinquish();
+    }
+  }
+  pdl_begin();
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();   // both CTAs' barriers are initialised before any remote signal
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      int last_par[kGemmStagesMax];
+      for (int s = 0; s < kGemmStagesMax; ++s) last_par[s] = -1;
+      const uint32_t full_leader = kPair ? cluster_addr(&sm->full[0], 0) : 0u;   // + 8 * stage
+      bool ok = p.test_stall == 0;
+      for (int w = first; w < units && ok; w += step) {
+        const LinUnit u = lin_unit(p, w);
+        const int row_x = (u.m * L::kCtas + (int)rank) * 128, row_w = u.n * L::kBN + (int)rank * (L::kBN / L::kCtas);
+        for (int kb = u.k0; kb < u.k1; ++kb) {
+          if (!mbar_wait(&sm->empty[st], ph ^ 1, abort, p.ew, 511)) {
+            ok = false;
+            break;
+          }
+          last_par[st] = (int)ph;
+          uint8_t* sa = smem + st * L::kStage;
+          if (leader) mbar_arrive_expect_tx(&sm->full[st], L::kCtas * L::kStage);   // whole boxes: zeros outside
+          if (kPair) {
+            tma_load_2d_pair(sa, &map_x, full_leader + 8u * st, kb * 64, row_x);
+            tma_load_2d_pair(sa + L::kABytes, &map_w, full_leader + 8u * st, kb * 64, row_w);
+          } else {
+            tma_load_2d(sa, &map_x, &sm->full[st], kb * 64, row_x);
+            tma_load_2d(sa + L::kABytes, &map_w, &sm->full[st], kb * 64, row_w);
+          }
+          if (++st == p.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (*abort && leader)   // let every load already issued land before the CTA can exit
+        for (int s = 0; s < p.stages; ++s)
+          if (last_par[s] >= 0) mbar_wait(&sm->full[s], last_par[s], nullptr, nullptr, 0, 200000000LL);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_bf16_f32(128 * L::kCtas, L::kBN);
+      int st = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      for (int w = first; w < units && ok; w += step) {
+        const LinUnit u = lin_unit(p, w);
+        if (!mbar_wait(&sm->acc_empty[acc], acc_ph ^ 1, abort, p.ew, 512)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * L::kBN;
+        for (int kb = u.k0; kb < u.k1; ++kb) {
+          if (!mbar_wait(&sm->full[st], ph, abort, p.ew, 513)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + st * L::kStage);
+          const uint64_t a = sdesc_kmajor_sw128(sa), b = sdesc_kmajor_sw128(sa + L::kABytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t accumulate = kb != u.k0 || kk != 0;
+            if (kPair) umma_bf16_pair(d, a + 2 * kk, b + 2 * kk, idesc, accumulate);
+            else umma_bf16(d, a + 2 * kk, b + 2 * kk, idesc, accumulate);
+          }
+          if (kPair) umma_commit_pair_both(&sm->empty[st]);
+          else umma_commit(&sm->empty[st]);
+          if (++st == p.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (kPair) umma_commit_pair_both(&sm->acc_full[acc]);
+        else umma_commit(&sm->acc_full[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_ph ^= 1;
+        }
+      }
+      if (!ok) {
+        if (kPair) umma_commit_pair(&sm->drain);
+        else umma_commit(&sm->drain);
+        mbar_wait(&sm->drain, 0, nullptr, nullptr, 0, 200000000LL);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, part = (warp - 2) >> 2;   // TMEM lane quadrant; 32-column blocks part, part + 2, ...
+    const int eid = threadIdx.x - 64;
+    float* stage = sm->stage[warp - 2];
+    const uint32_t acc_empty_leader = kPair ? cluster_addr(&sm->acc_empty[0], 0) : 0u;   // + 8 * buffer
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    for (int w = first; w < units; w += step) {
+      const LinUnit u = lin_unit(p, w);
+      // with cut tiles a CTA has one unit, and its warps meet at barriers below even after an abort
+      const bool have = mbar_wait_warp(&sm->acc_full[acc], acc_ph, abort, p.ew, 514);
+      if (!have && p.splits == 1) break;
+      (void)mbar_try_wait(&sm->acc_full[acc], acc_ph);   // every lane observes the completed phase
+      tc_fence_after();
+      const uint32_t taddr = tmem + acc * L::kBN + ((uint32_t)(q * 32) << 16);
+      const int row0 = (u.m * L::kCtas + (int)rank) * 128 + q * 32;   // the warp's first token
+      const long col0 = (long)u.n * L::kBN;
+      constexpr int kBlocks = L::kBN / 32;
+      // partials: [unit][CTA of the pair][column][128 rows]
+      constexpr int kPart = L::kBN * 128;
+      float* part_base = p.scratch + (((size_t)u.tile * p.splits) * L::kCtas + rank) * kPart + q * 32 + lane;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair) mbar_arrive_remote(acc_empty_leader + 8u * acc);
+          else mbar_arrive(&sm->acc_empty[acc]);
+        }
+      };
+      bool finish = true;
+      if (p.splits > 1) {
+        float* mine = part_base + (size_t)u.split * L::kCtas * kPart;
+        for (int blk = part; blk < kBlocks && have; blk += 2) {
+          float v[2][16];
+          tmem_ld16(taddr + blk * 32, v[0]);
+          tmem_ld16(taddr + blk * 32 + 16, v[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(mine + (blk * 32 + i) * 128, v[i >> 4][i & 15]);
+        }
+        release();
+        __threadfence();
+        epilogue_sync();
+        if (eid == 0) {
+          int* done = &p.ew->linear_done[u.tile * L::kCtas + (int)rank];
+          const int last = atomicAdd(done, 1) == p.splits - 1;
+          if (last) *done = 0;
+          __threadfence();
+          sm->last = last;
+        }
+        epilogue_sync();
+        finish = sm->last != 0;
+        epilogue_sync();   // before the next unit's flag
+      }
+      if (finish) {
+        for (int blk = part; blk < kBlocks; blk += 2) {
+          const long c = col0 + blk * 32;
+          if (row0 >= p.T || c >= p.N) break;   // warp-uniform: nothing of this block (or later ones) is kept
+          float v[2][16];
+          if (p.splits == 1) {
+            tmem_ld16(taddr + blk * 32, v[0]);
+            tmem_ld16(taddr + blk * 32 + 16, v[1]);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] = 0.f;
+            for (int s = 0; s < p.splits; ++s) {
+              const float* src = part_base + (size_t)s * L::kCtas * kPart + blk * 32 * 128;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] += __ldcg(src + i * 128);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) stage[lane * kEpiPitch + i] = v[i >> 4][i & 15];
+          __syncwarp();
+          const long c8 = c + (lane & 3) * 8;
+          float b[8];
+          load_bias8(p, c8, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            if (row0 + r < p.T && c8 < p.N) {
+              float z[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) z[j] = stage[r * kEpiPitch + (lane & 3) * 8 + j];
+              finish8(p, row0 + r, c8, z, b);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (p.splits == 1) release();
+      if (++acc == 2) {
+        acc = 0;
+        acc_ph ^= 1;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();  // no remote signal or MMA of either CTA is outstanding past this point
+  if (*abort) {
+    // a wait ran out: give any TMA copy this CTA may still have in flight time to land
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000LL) {
+    }
+  }
+  tc_fence_after();
+  if (warp == 1) {
+    if (kPair) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kPair>
+cudaError_t launch_gemm(const CUtensorMap& map_x, const CUtensorMap& map_w, LinearParams p, int num_sms,
+                        cudaStream_t stream) {
+  using L = LinTile<kPair>;
+  auto kernel = linear_gemm_kernel<kPair>;
+  p.stages = (int)std::min<size_t>(kGemmStagesMax, (227 * 1024 - 1024 - sizeof(LinGemmSmem)) / L::kStage);
+  const size_t smem = 1024 + p.stages * (size_t)L::kStage + sizeof(LinGemmSmem);
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const int units = p.m_tiles * p.n_tiles * p.splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L::kCtas * (num_sms / L::kCtas));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  int slots = num_sms / L::kCtas, active = 0;
+  if (kPair && cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) == cudaSuccess && active > 0 && active < slots)
+    slots = active;
+  (void)cudaGetLastError();
+  cfg.gridDim = dim3(L::kCtas * std::min(units, slots));
+  cfg.numAttrs = n + pdl_attr(attr + n);
+  return cudaLaunchKernelEx(&cfg, kernel, map_x, map_w, p);
+}
+
+template <int kNT>
+cudaError_t launch_stream(const CUtensorMap& map_w, LinearParams p, int num_sms, cudaStream_t stream) {
+  auto kernel = linear_stream_kernel<kNT>;
+  p.stages = (int)std::min<size_t>(kStreamMaxStages, (227 * 1024 - 1024 - sizeof(StreamSmem<kNT>)) / kStreamBytes) & ~1;
+  const size_t smem = 1024 + (size_t)p.stages * kStreamBytes + sizeof(StreamSmem<kNT>);
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const long U = (long)((p.N + kStreamRows - 1) / kStreamRows) * ((p.K + kStreamK - 1) / kStreamK);
+  return launch_pdl(kernel, dim3((unsigned)std::min<long>(num_sms, U)), dim3(kStreamThreads), smem, stream, map_w, p);
+}
+
+}  // namespace
+
+LinearPlan linear_plan(int T, int K, int N, int num_sms) {
+  LinearPlan plan{};
+  if (T <= kLinearStreamTokens) {
+    plan.kind = LinearPlan::kStream;
+    plan.w_box = kStreamRows;
+    plan.scratch_floats = (size_t)num_sms * 2 * kStreamRows * 16;
+    return plan;
+  }
+  // Time of a choice in units of 64 elements of k on one SM: a step costs the larger of its MMAs (one unit
+  // for 128 x 256 x 64 per SM) and its loads (32 KB a unit), a unit of work also its epilogue and pipeline
+  // fill.
+  const long nk = (K + 63) / 64;
+  double best = 0;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int rows = pair ? 256 : 128, cols = pair ? 256 : 128, slots = pair ? num_sms / 2 : num_sms;
+    const long m = ((long)T + rows - 1) / rows, n = ((long)N + cols - 1) / cols;
+    const double loads = pair ? 1.0 : 0.5 * (std::min(T, 128) / 128.0) + 0.5, mma = pair ? 1.0 : 0.5;
+    for (int s = 1; s <= 16 && s <= nk; ++s) {
+      if (s > 1 && m * n * s > slots) break;   // K is cut only to fill the SMs once
+      const long units = m * n * s, waves = (units + slots - 1) / slots;
+      const double unit = ((nk + s - 1) / s) * std::max(loads, mma) + (pair ? 12 : 8) + (s > 1 ? 4 + 2 * s : 0);
+      const double cost = waves * unit;
+      if (best == 0 || cost < best) {
+        best = cost;
+        plan.kind = pair ? LinearPlan::kPair : LinearPlan::kSolo;
+        plan.m_tiles = (int)m;
+        plan.n_tiles = (int)n;
+        plan.splits = s;
+        plan.w_box = 128;
+        plan.scratch_floats = s > 1 ? (size_t)units * rows * cols : 0;
+      }
+    }
+  }
+  return plan;
+}
+
+cudaError_t launch_linear(const LinearPlan& plan, const CUtensorMap& map_x, const CUtensorMap& map_w, LinearParams p,
+                          int num_sms, cudaStream_t stream) {
+  p.m_tiles = plan.m_tiles;
+  p.n_tiles = plan.n_tiles;
+  p.splits = plan.splits;
+  if (plan.kind == LinearPlan::kStream)
+    return p.T <= 8 ? launch_stream<1>(map_w, p, num_sms, stream) : launch_stream<2>(map_w, p, num_sms, stream);
+  return plan.kind == LinearPlan::kPair ? launch_gemm<true>(map_x, map_w, p, num_sms, stream)
+                                        : launch_gemm<false>(map_x, map_w, p, num_sms, stream);
+}
+
+}  // namespace moe

@@ -252,6 +252,19 @@ bool make_map_columns(CUtensorMap* map, const void* base, uint64_t rows, uint64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// T or N rows of `cols` bf16 at stride `ld` elements, boxes of [box_rows, 64] (128-byte swizzle).
+bool make_map_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 #define MOE_TRY(expr)                      \
@@ -905,6 +918,20 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   return cuda_status(moe::launch_layer_decode(m1, m3, m2, p, fp4 != nullptr, num_sms(), s));
 }
 
+moe_status check_linear(const moe_linear_desc* d, int T) {
+  if (d == nullptr || T < 0 || d->in_features <= 0 || d->out_features <= 0) return MOE_ERR_INVALID;
+  if (d->activation < MOE_ACT_NONE || d->activation > MOE_ACT_GELU_TANH || (d->out_fp32 != 0 && d->out_fp32 != 1))
+    return MOE_ERR_INVALID;
+  if (d->in_features % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The linear projection's workspace: the control words, then the partials of cut tiles.
+size_t linear_ws_bytes(const moe_linear_desc& d, int T) {
+  const moe::LinearPlan plan = moe::linear_plan(T, d.in_features, d.out_features, num_sms());
+  return align_up(sizeof(ErrorWord)) + align_up(plan.scratch_floats * sizeof(float));
+}
+
 }  // namespace
 
 // =============================================================================================
@@ -1112,6 +1139,49 @@ moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x
   if (weights_mxfp4 == nullptr) return MOE_ERR_INVALID;
   return decode_impl(desc, T, x, token_ids, tid2eid, vocab, w_gate, bias, logit_offset, nullptr, nullptr, nullptr,
                      weights_mxfp4, y, weights_out, indices_out, counts_out, ws, ws_bytes, stream);
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc, int T) {
+  if (check_linear(desc, T) != MOE_OK) return 0;
+  return linear_ws_bytes(*desc, T);
+}
+
+moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int64_t ldx, const moe_bf16* w,
+                      const float* bias, const moe_bf16* residual, int64_t ldr, void* y, int64_t ldy, void* ws,
+                      size_t ws_bytes, moe_stream_t stream) {
+  NvtxRange nvtx("moe_linear");
+  MOE_TRY(check_linear(desc, T));
+  const moe_linear_desc& d = *desc;
+  const int K = d.in_features, N = d.out_features;
+  if (ldx < K || ldy < N || (residual != nullptr && ldr < N)) return MOE_ERR_INVALID;
+  if (ldx % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (ldx >= (int64_t(1) << 38)) return MOE_ERR_UNSUPPORTED;   // a tensor map's stride is below 2^40 bytes
+  auto misaligned = [](const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) != 0; };
+  if (T > 0 && (x == nullptr || w == nullptr || y == nullptr)) return MOE_ERR_INVALID;
+  if (T > 0 && (!aligned16(x) || !aligned16(w) || misaligned(y, d.out_fp32 ? 4 : 2) || misaligned(bias, 4) ||
+                misaligned(residual, 2)))
+    return MOE_ERR_INVALID;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_WORKSPACE;
+  const int sms = num_sms();
+  const moe::LinearPlan plan = moe::linear_plan(T, K, N, sms);
+  if (ws_bytes < align_up(sizeof(ErrorWord)) + align_up(plan.scratch_floats * sizeof(float))) return MOE_ERR_WORKSPACE;
+  if (T == 0) return MOE_OK;
+  moe::LinearParams p{};
+  p.T = T; p.K = K; p.N = N; p.act = d.activation; p.out_fp32 = d.out_fp32;
+  p.ldx = ldx; p.ldy = ldy; p.ldr = ldr;
+  p.y_vec = aligned16(y) && ldy % (d.out_fp32 ? 4 : 8) == 0;
+  p.residual_vec = aligned16(residual) && ldr % 8 == 0;
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.bias = bias;
+  p.residual = reinterpret_cast<const __nv_bfloat16*>(residual);
+  p.y = y;
+  p.scratch = at<float>(ws, align_up(sizeof(ErrorWord)));
+  p.ew = at<ErrorWord>(ws, 0);
+  p.test_stall = test_stall_flag();
+  CUtensorMap mx{}, mw;
+  if (plan.kind != moe::LinearPlan::kStream && !make_map_rows(&mx, x, T, K, ldx, 128)) return MOE_ERR_CUDA;
+  if (!make_map_rows(&mw, w, N, K, K, plan.w_box)) return MOE_ERR_CUDA;
+  return cuda_status(moe::launch_linear(plan, mx, mw, p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_get_error(void* ws, moe_stream_t stream, int32_t* info) {

@@ -69,10 +69,27 @@ class Mxfp4Weights(ctypes.Structure):
                 ("w3_scale", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int), ("out_features", ctypes.c_int), ("activation", ctypes.c_int),
+                ("out_fp32", ctypes.c_int)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def linear_desc(in_features: int, out_features: int, activation: str = "none",
+                out_dtype: torch.dtype = torch.bfloat16) -> LinearDesc:
+    """moe_linear_desc of a projection; out_dtype is torch.bfloat16 or torch.float32."""
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    return LinearDesc(int(in_features), int(out_features), ACTIVATIONS[activation], int(out_dtype == torch.float32))
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _D = ctypes.POINTER(LayerDesc)
 _W4 = ctypes.POINTER(Mxfp4Weights)
+_L = ctypes.POINTER(LinearDesc)
 _SIG = {
     "moe_workspace_bytes": (ctypes.c_size_t, [_D, _I]),
     "moe_workspace_init": (_I, [_P, ctypes.c_size_t, _P]),
@@ -98,6 +115,9 @@ _SIG = {
     "moe_forward_mxfp4": (_I, [_D, _I, _P, _P, _P, _I, _P, _P, _P, _W4, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_decode": (_I, [_D, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_decode_mxfp4": (_I, [_D, _I, _P, _P, _P, _I, _P, _P, _P, _W4, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_linear_workspace_bytes": (ctypes.c_size_t, [_L, _I]),
+    "moe_linear": (_I, [_L, _I, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_size_t,
+                        _P]),
     "moe_update_bias": (_I, [_D, _I, _P, _P, ctypes.c_float, _P]),
     "moe_get_error": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "moe_status_str": (ctypes.c_char_p, [_I]),
@@ -159,11 +179,12 @@ def moe_workspace_bytes(desc: LayerDesc, T: int) -> int:
 
 class Workspace:
     """A device workspace of moe_workspace_bytes(desc, T) bytes (1 KiB aligned), error word cleared."""
+    _bytes = staticmethod(moe_workspace_bytes)
 
-    def __init__(self, desc: LayerDesc, T: int, device=None):
-        n = moe_workspace_bytes(desc, T)
+    def __init__(self, desc, T: int, device=None):
+        n = self._bytes(desc, T)
         if n == 0:
-            raise MoeError(MOE_ERR_INVALID, "moe_workspace_bytes")
+            raise MoeError(MOE_ERR_INVALID, f"moe_{'linear_' if isinstance(desc, LinearDesc) else ''}workspace_bytes")
         self.buf = torch.empty(n + 1024, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buf.data_ptr()) % 1024
         self.tensor = self.buf[off:off + n]
@@ -173,6 +194,15 @@ class Workspace:
     @property
     def ptr(self) -> int:
         return self.tensor.data_ptr()
+
+
+def moe_linear_workspace_bytes(desc: LinearDesc, T: int) -> int:
+    return int(lib.moe_linear_workspace_bytes(ctypes.byref(desc), T))
+
+
+class LinearWorkspace(Workspace):
+    """A device workspace of moe_linear_workspace_bytes(desc, T) bytes, cleared."""
+    _bytes = staticmethod(moe_linear_workspace_bytes)
 
 
 def moe_workspace_init(ws: Workspace, stream=None):
@@ -448,6 +478,30 @@ def moe_decode_mxfp4(desc, x, w_gate, w, y, ws: Workspace, bias=None, logit_offs
                                 _ptr(w_gate), _ptr(bias), _ptr(logit_offset), ctypes.byref(mw), _ptr(y),
                                 _ptr(weights_out), _ptr(indices_out), _ptr(counts_out), ws.ptr, ws.nbytes,
                                 _stream(stream)), "moe_decode_mxfp4")
+
+
+def _rows(t: torch.Tensor, dtype, T: int, cols: int, name: str, device: int) -> int:
+    """Checks T rows of cols contiguous elements; returns their stride (whatever it is for a single row)."""
+    _shape(t, dtype, (T, cols), name, device)
+    ld, inner = t.stride()
+    if (inner != 1 and cols > 1) or (ld < cols and T > 1):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return ld if T > 1 else (cols + 7) // 8 * 8
+
+
+def moe_linear(desc: LinearDesc, x, w, y, ws: LinearWorkspace, bias=None, residual=None, stream=None):
+    """y = act(x w^T + bias) + residual.  x [T, K], y and residual [T, N] may be rows of wider tensors; y may be
+    residual itself."""
+    dev = torch.cuda.current_device()
+    T, K, N = x.shape[0], desc.in_features, desc.out_features
+    ldx = _rows(x, torch.bfloat16, T, K, "x", dev)
+    ldy = _rows(y, torch.float32 if desc.out_fp32 else torch.bfloat16, T, N, "y", dev)
+    ldr = 0 if residual is None else _rows(residual, torch.bfloat16, T, N, "residual", dev)
+    _shape(w, torch.bfloat16, (N, K), "w", dev)
+    _shape(bias, torch.float32, (N,), "bias", dev)
+    _check(lib.moe_linear(ctypes.byref(desc), T, x.data_ptr(), ldx, _ptr(w), _ptr(bias),
+                          None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, ws.ptr, ws.nbytes,
+                          _stream(stream)), "moe_linear")
 
 
 def moe_get_error(ws: Workspace, stream=None):

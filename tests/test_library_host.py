@@ -384,3 +384,43 @@ def test_decode_rejects_bad_arguments_before_launch(moe):
     assert moe.lib.moe_decode_mxfp4(*args(d, ctypes.byref(w))) == moe.MOE_ERR_INVALID
     w.w2_scale = (1 << 20) + 4
     assert moe.lib.moe_decode_mxfp4(*args(d, ctypes.byref(w))) == moe.MOE_ERR_INVALID
+
+
+def test_linear_rejects_bad_arguments_before_launch(moe):
+    P = ctypes.c_void_p
+    fake = P(1 << 20)   # never dereferenced: every call must fail its checks first
+
+    def call(desc=None, T=4, x=fake, ldx=64, w=fake, bias=None, res=None, ldr=32, y=fake, ldy=32, ws=fake, n=1 << 30):
+        d = desc or moe.linear_desc(64, 32)
+        return moe.lib.moe_linear(ctypes.byref(d), T, x, ldx, w, bias, res, ldr, y, ldy, ws, n, None)
+
+    import torch
+    assert moe.moe_linear_workspace_bytes(moe.linear_desc(64, 32), 4) > 0
+    assert moe.moe_linear_workspace_bytes(moe.linear_desc(64, 32), -1) == 0
+    assert moe.moe_linear_workspace_bytes(moe.linear_desc(60, 32), 4) == 0
+    assert call(T=-1) == moe.MOE_ERR_INVALID
+    assert call(desc=moe.linear_desc(0, 32)) == moe.MOE_ERR_INVALID
+    assert call(desc=moe.linear_desc(64, 0)) == moe.MOE_ERR_INVALID
+    assert call(desc=moe.linear_desc(60, 32)) == moe.MOE_ERR_UNSUPPORTED
+    for field, v in (("activation", 5), ("activation", -1), ("out_fp32", 2)):
+        d = moe.linear_desc(64, 32)
+        setattr(d, field, v)
+        assert call(desc=d) == moe.MOE_ERR_INVALID
+    assert call(ldx=63) == moe.MOE_ERR_INVALID and call(ldx=68) == moe.MOE_ERR_UNSUPPORTED
+    assert call(ldx=1 << 39) == moe.MOE_ERR_UNSUPPORTED
+    assert call(ldy=31) == moe.MOE_ERR_INVALID and call(res=fake, ldr=31) == moe.MOE_ERR_INVALID
+    for name in ("x", "w", "y"):
+        assert call(**{name: None}) == moe.MOE_ERR_INVALID, name
+        assert call(**{name: P((1 << 20) + 1)}) == moe.MOE_ERR_INVALID, name
+    for name in ("x", "w"):
+        assert call(**{name: P((1 << 20) + 8)}) == moe.MOE_ERR_INVALID, name
+    assert call(bias=P((1 << 20) + 2)) == moe.MOE_ERR_INVALID
+    assert call(res=P((1 << 20) + 1)) == moe.MOE_ERR_INVALID
+    f32 = moe.linear_desc(64, 32, out_dtype=torch.float32)
+    assert call(desc=f32, y=P((1 << 20) + 2)) == moe.MOE_ERR_INVALID
+    assert call(ws=None) == moe.MOE_ERR_WORKSPACE and call(n=1024) == moe.MOE_ERR_WORKSPACE
+    assert call(ws=P((1 << 20) + 64)) == moe.MOE_ERR_WORKSPACE
+    with pytest.raises(ValueError):
+        moe.linear_desc(64, 32, out_dtype=torch.float16)
+    with pytest.raises(KeyError):
+        moe.linear_desc(64, 32, activation="tanh")
