@@ -77,6 +77,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A warp's arrival after it has read a shared-memory stage with plain loads, which frees the stage for the
+// next TMA copy.  Every lane's reads are fenced first: without the fence a weight-stream kernel read rows of
+// the next fill (seen as wrong rows in about one launch of six, in the stage behind a tile's end).
+__device__ __forceinline__ void mbar_arrive_after_reads(uint64_t* bar) {
+  __threadfence_block();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(

@@ -989,8 +989,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, cur, acc, p.ew);
           }
           if (!kEarly && s + 2 < ns) fetch(s + 2);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->empty[mine.slot]);
+          mbar_arrive_after_reads(&sm->empty[mine.slot]);
         }
         count += ns;
         pos.step(ns, p.stages);

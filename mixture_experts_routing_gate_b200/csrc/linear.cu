@@ -218,8 +218,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             mma_16816(acc[i][nt], lo.z, hi.z, lo.w, hi.w, cur[nt].z, cur[nt].w);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->empty[slot]);
+        mbar_arrive_after_reads(&sm->empty[slot]);
         slot += 2;
         if (slot >= p.stages) {
           slot -= p.stages;
@@ -357,7 +356,12 @@ __device__ __forceinline__ LinUnit lin_unit(const LinearParams& p, int w) {
   return u;
 }
 
-template <bool kPair>
+// kPromote (fp32 outputs): the tensor cores add into the fp32 accumulator with truncation, a bias that grows
+// with the number of steps -- 8e-6 of the result after 7168 products.  So K is accumulated in chunks of
+// kPromoteSteps * 64, alternating between the two accumulators, and the epilogue warps add the chunks in
+// registers, rounding to nearest.
+constexpr int kPromoteSteps = 8;
+template <bool kPair, bool kPromote>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ LinearParams p) {
@@ -446,15 +450,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int st = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
+      auto finish_acc = [&]() {
+        if (kPair) umma_commit_pair_both(&sm->acc_full[acc]);
+        else umma_commit(&sm->acc_full[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_ph ^= 1;
+        }
+      };
       for (int w = first; w < units && ok; w += step) {
         const LinUnit u = lin_unit(p, w);
-        if (!mbar_wait(&sm->acc_empty[acc], acc_ph ^ 1, abort, p.ew, 512)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * L::kBN;
+        uint32_t d = 0;
         for (int kb = u.k0; kb < u.k1; ++kb) {
+          const bool start = kb == u.k0 || (kPromote && (kb - u.k0) % kPromoteSteps == 0);
+          if (start) {   // a new accumulator
+            if (kb != u.k0) finish_acc();
+            if (!mbar_wait(&sm->acc_empty[acc], acc_ph ^ 1, abort, p.ew, 512)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            d = tmem + acc * L::kBN;
+          }
           if (!mbar_wait(&sm->full[st], ph, abort, p.ew, 513)) {
             ok = false;
             break;
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const uint64_t a = sdesc_kmajor_sw128(sa), b = sdesc_kmajor_sw128(sa + L::kABytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t accumulate = kb != u.k0 || kk != 0;
+            const uint32_t accumulate = !start || kk != 0;
             if (kPair) umma_bf16_pair(d, a + 2 * kk, b + 2 * kk, idesc, accumulate);
             else umma_bf16(d, a + 2 * kk, b + 2 * kk, idesc, accumulate);
           }
@@ -476,12 +493,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
         if (!ok) break;
-        if (kPair) umma_commit_pair_both(&sm->acc_full[acc]);
-        else umma_commit(&sm->acc_full[acc]);
-        if (++acc == 2) {
-          acc = 0;
-          acc_ph ^= 1;
-        }
+        finish_acc();
       }
       if (!ok) {
         if (kPair) umma_commit_pair(&sm->drain);
@@ -500,18 +512,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint32_t acc_ph = 0;
     for (int w = first; w < units; w += step) {
       const LinUnit u = lin_unit(p, w);
-      // with cut tiles a CTA has one unit, and its warps meet at barriers below even after an abort
-      const bool have = mbar_wait_warp(&sm->acc_full[acc], acc_ph, abort, p.ew, 514);
-      if (!have && p.splits == 1) break;
-      (void)mbar_try_wait(&sm->acc_full[acc], acc_ph);   // every lane observes the completed phase
-      tc_fence_after();
-      const uint32_t taddr = tmem + acc * L::kBN + ((uint32_t)(q * 32) << 16);
-      const int row0 = (u.m * L::kCtas + (int)rank) * 128 + q * 32;   // the warp's first token
-      const long col0 = (long)u.n * L::kBN;
-      constexpr int kBlocks = L::kBN / 32;
-      // partials: [unit][CTA of the pair][column][128 rows]
-      constexpr int kPart = L::kBN * 128;
-      float* part_base = p.scratch + (((size_t)u.tile * p.splits) * L::kCtas + rank) * kPart + q * 32 + lane;
+      uint32_t taddr = 0;
+      auto await_acc = [&]() {
+        const bool got = mbar_wait_warp(&sm->acc_full[acc], acc_ph, abort, p.ew, 514);
+        (void)mbar_try_wait(&sm->acc_full[acc], acc_ph);   // every lane observes the completed phase
+        tc_fence_after();
+        taddr = tmem + acc * L::kBN + ((uint32_t)(q * 32) << 16);
+        return got;
+      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -519,19 +527,57 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (kPair) mbar_arrive_remote(acc_empty_leader + 8u * acc);
           else mbar_arrive(&sm->acc_empty[acc]);
         }
+        if (++acc == 2) {
+          acc = 0;
+          acc_ph ^= 1;
+        }
       };
+      auto load_block = [&](int blk, float (&v)[32]) {
+        tmem_ld16(taddr + blk * 32, *reinterpret_cast<float(*)[16]>(&v[0]));
+        tmem_ld16(taddr + blk * 32 + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
+        tmem_ld_wait();
+      };
+      constexpr int kMine = L::kBN / 64;   // 32-column blocks of this warp
+      float sum[kPromote ? kMine : 1][32];
+      // with cut tiles a CTA has one unit, and its warps meet at barriers below even after an abort
+      bool have = await_acc();
+      if constexpr (kPromote) {
+        const int chunks = (u.k1 - u.k0 + kPromoteSteps - 1) / kPromoteSteps;
+#pragma unroll
+        for (int b = 0; b < kMine; ++b)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[b][i] = 0.f;
+        for (int c = 0; c < chunks && have; ++c) {
+          if (c > 0) have = await_acc();
+#pragma unroll
+          for (int b = 0; b < kMine; ++b) {
+            float v[32];
+            load_block(part + 2 * b, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[b][i] += v[i];
+          }
+          release();
+        }
+      }
+      if (!have && p.splits == 1) break;
+      const int row0 = (u.m * L::kCtas + (int)rank) * 128 + q * 32;   // the warp's first token
+      const long col0 = (long)u.n * L::kBN;
+      // partials: [unit][CTA of the pair][column][128 rows]
+      constexpr int kPart = L::kBN * 128;
+      float* part_base = p.scratch + (((size_t)u.tile * p.splits) * L::kCtas + rank) * kPart + q * 32 + lane;
       bool finish = true;
       if (p.splits > 1) {
         float* mine = part_base + (size_t)u.split * L::kCtas * kPart;
-        for (int blk = part; blk < kBlocks && have; blk += 2) {
-          float v[2][16];
-          tmem_ld16(taddr + blk * 32, v[0]);
-          tmem_ld16(taddr + blk * 32 + 16, v[1]);
-          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) __stcg(mine + (blk * 32 + i) * 128, v[i >> 4][i & 15]);
+        for (int b = 0; b < kMine; ++b) {
+          if (!have) break;
+          const int blk = part + 2 * b;
+          float v[32];
+          if constexpr (!kPromote) load_block(blk, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(mine + (blk * 32 + i) * 128, kPromote ? sum[kPromote ? b : 0][i] : v[i]);
         }
-        release();
+        if (!kPromote) release();
         __threadfence();
         epilogue_sync();
         if (eid == 0) {
@@ -546,29 +592,34 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         epilogue_sync();   // before the next unit's flag
       }
       if (finish) {
-        for (int blk = part; blk < kBlocks; blk += 2) {
+#pragma unroll
+        for (int b = 0; b < kMine; ++b) {
+          const int blk = part + 2 * b;
           const long c = col0 + blk * 32;
           if (row0 >= p.T || c >= p.N) break;   // warp-uniform: nothing of this block (or later ones) is kept
-          float v[2][16];
+          float v[32];
           if (p.splits == 1) {
-            tmem_ld16(taddr + blk * 32, v[0]);
-            tmem_ld16(taddr + blk * 32 + 16, v[1]);
-            tmem_ld_wait();
+            if constexpr (kPromote) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = sum[b][i];
+            } else {
+              load_block(blk, v);
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] = 0.f;
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
             for (int s = 0; s < p.splits; ++s) {
               const float* src = part_base + (size_t)s * L::kCtas * kPart + blk * 32 * 128;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] += __ldcg(src + i * 128);
+              for (int i = 0; i < 32; ++i) v[i] += __ldcg(src + i * 128);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) stage[lane * kEpiPitch + i] = v[i >> 4][i & 15];
+          for (int i = 0; i < 32; ++i) stage[lane * kEpiPitch + i] = v[i];
           __syncwarp();
           const long c8 = c + (lane & 3) * 8;
-          float b[8];
-          load_bias8(p, c8, b);
+          float b8[8];
+          load_bias8(p, c8, b8);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = (lane >> 2) + 8 * i;
@@ -576,17 +627,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               float z[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) z[j] = stage[r * kEpiPitch + (lane & 3) * 8 + j];
-              finish8(p, row0 + r, c8, z, b);
+              finish8(p, row0 + r, c8, z, b8);
             }
           }
           __syncwarp();
         }
       }
-      if (p.splits == 1) release();
-      if (++acc == 2) {
-        acc = 0;
-        acc_ph ^= 1;
-      }
+      if (p.splits == 1 && !kPromote) release();
     }
   }
 
@@ -606,11 +653,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-template <bool kPair>
+template <bool kPair, bool kPromote>
 cudaError_t launch_gemm(const CUtensorMap& map_x, const CUtensorMap& map_w, LinearParams p, int num_sms,
                         cudaStream_t stream) {
   using L = LinTile<kPair>;
-  auto kernel = linear_gemm_kernel<kPair>;
+  auto kernel = linear_gemm_kernel<kPair, kPromote>;
   p.stages = (int)std::min<size_t>(kGemmStagesMax, (227 * 1024 - 1024 - sizeof(LinGemmSmem)) / L::kStage);
   const size_t smem = 1024 + p.stages * (size_t)L::kStage + sizeof(LinGemmSmem);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -697,8 +744,11 @@ cudaError_t launch_linear(const LinearPlan& plan, const CUtensorMap& map_x, cons
   p.splits = plan.splits;
   if (plan.kind == LinearPlan::kStream)
     return p.T <= 8 ? launch_stream<1>(map_w, p, num_sms, stream) : launch_stream<2>(map_w, p, num_sms, stream);
-  return plan.kind == LinearPlan::kPair ? launch_gemm<true>(map_x, map_w, p, num_sms, stream)
-                                        : launch_gemm<false>(map_x, map_w, p, num_sms, stream);
+  if (plan.kind == LinearPlan::kPair)
+    return p.out_fp32 ? launch_gemm<true, true>(map_x, map_w, p, num_sms, stream)
+                      : launch_gemm<true, false>(map_x, map_w, p, num_sms, stream);
+  return p.out_fp32 ? launch_gemm<false, true>(map_x, map_w, p, num_sms, stream)
+                    : launch_gemm<false, false>(map_x, map_w, p, num_sms, stream);
 }
 
 }  // namespace moe

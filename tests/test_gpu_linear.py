@@ -83,6 +83,21 @@ def test_stream(M, T, K, N):
     _run(M, T, K, N, ACTS[(T + N) % 5], bias=T % 2 == 0, residual=N % 2 == 1, xpad=8 * (T % 3), ypad=T % 4)
 
 
+@pytest.mark.parametrize("T", [1, 16])
+def test_stream_with_a_full_ring_behind_every_tile(M, T):
+    # each CTA's run crosses a tile's end while the weight ring is full behind it: warps that are late with
+    # the next tile's first stage must still find it
+    K = N = 7168
+    x, w = _normal((T, K), 1.0, 3), _normal((N, K), 1.0 / math.sqrt(K), 4)
+    desc = M.linear_desc(K, N, out_dtype=torch.float32)
+    ws = M.LinearWorkspace(desc, T)
+    outs = [torch.empty((T, N), dtype=torch.float32, device="cuda") for _ in range(60)]
+    for y in outs:
+        M.moe_linear(desc, x, w, y, ws)
+    _check(outs[0], x, w, "none", None, None)
+    assert all(torch.equal(y, outs[0]) for y in outs)
+
+
 @pytest.mark.parametrize("T", [17, 33, 64, 127, 128, 129, 300, 513])
 @pytest.mark.parametrize("K,N", [(8, 1), (64, 128), (72, 130), (1000, 255), (2048, 257), (512, 1536), (7168, 40)])
 def test_tiles(M, T, K, N):
