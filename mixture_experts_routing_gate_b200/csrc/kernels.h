@@ -188,7 +188,7 @@ constexpr int kLinearStreamTokens = 16;   // batches up to this run as a weight 
 struct LinearParams {
   int T, K, N;
   int act, out_fp32;
-  int y_vec, residual_vec;    // rows of y / residual start on 16-byte boundaries
+  int y_vec, residual_vec, bias_vec;  // rows of y / residual, and bias, start on 16-byte boundaries
   int stages;                 // set by the launcher
   int m_tiles, n_tiles, splits;
   int test_stall;
@@ -200,8 +200,8 @@ struct LinearParams {
   float* scratch;
   ErrorWord* ew;
 };
-// How a projection of T tokens runs: as a weight stream, or in tiles of single CTAs or CTA pairs with K cut
-// into `splits`.  w_box: weight rows per box of its tensor map (64 elements of k wide).
+// How a projection of T tokens runs: as a weight stream, or in tiles of CTA pairs or of single CTAs, these with
+// K cut over a cluster of `splits`.  w_box: weight rows per box of its tensor map (64 elements of k wide).
 struct LinearPlan {
   enum Kind { kStream, kSolo, kPair } kind;
   int m_tiles, n_tiles, splits;

@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -22,31 +23,52 @@ namespace {
 // ------------------------------------------------------------------------------------------------
 // NaN goes through every branch.  silu and the tanh form of gelu are z / (1 + e^-a) (no cancellation for
 // negative z); the exact gelu uses erfc for the same reason.
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (act == MOE_ACT_SILU) return __fdiv_rn(z, 1.f + __expf(-z));
-  if (act == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
-  if (act == MOE_ACT_GELU_TANH) return __fdiv_rn(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+template <int kAct>
+__device__ __forceinline__ float activate(float z) {
+  if (kAct == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
+  if (kAct == MOE_ACT_SILU) return __fdiv_rn(z, 1.f + __expf(-z));
+  if (kAct == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+  if (kAct == MOE_ACT_GELU_TANH) return __fdiv_rn(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
   return z;
 }
 
-// Eight consecutive outputs (columns c .. c + 7 of row t) from their accumulators.
-__device__ __forceinline__ void finish8(const LinearParams& p, int t, long c, const float (&z)[8], const float (&bias)[8]) {
+// Eight consecutive outputs (columns c .. c + 7 of row t) in two steps, so that a caller can have the loads of
+// several under way: what the epilogue reads, then what it computes and writes.  Whole vectors where the rows
+// are aligned, single elements at the edge of N and elsewhere.
+__device__ __forceinline__ bool whole8(const LinearParams& p, long c) { return c + 8 <= p.N; }
+
+__device__ __forceinline__ void load_bias8(const LinearParams& p, long c, float (&b)[8]) {
+  if (p.bias != nullptr && p.bias_vec && whole8(p, c)) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p.bias + c)), y = __ldg(reinterpret_cast<const float4*>(p.bias + c) + 1);
+    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+    b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = p.bias != nullptr && c + i < p.N ? __ldg(p.bias + c + i) : 0.f;
+  }
+}
+__device__ __forceinline__ uint4 load_residual8(const LinearParams& p, int t, long c) {
+  if (p.residual == nullptr || !p.residual_vec || !whole8(p, c)) return make_uint4(0u, 0u, 0u, 0u);
+  return *reinterpret_cast<const uint4*>(p.residual + (size_t)t * p.ldr + c);
+}
+
+template <int kAct>
+__device__ __forceinline__ void finish8(const LinearParams& p, int t, long c, const float (&z)[8], const float (&bias)[8],
+                                        const uint4& res) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate(z[i] + bias[i], p.act);
-  const bool whole = c + 8 <= p.N;
+  for (int i = 0; i < 8; ++i) v[i] = activate<kAct>(z[i] + bias[i]);
+  const bool whole = whole8(p, c);
   if (p.residual != nullptr) {
-    const __nv_bfloat16* r = p.residual + (size_t)t * p.ldr + c;
     if (whole && p.residual_vec) {
-      const uint4 q = *reinterpret_cast<const uint4*>(r);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const uint32_t w[4] = {res.x, res.y, res.z, res.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] += __uint_as_float(w[i] << 16);
         v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
       }
     } else {
+      const __nv_bfloat16* r = p.residual + (size_t)t * p.ldr + c;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (c + i < p.N) v[i] += __bfloat162float(r[i]);
@@ -75,9 +97,16 @@ __device__ __forceinline__ void finish8(const LinearParams& p, int t, long c, co
   }
 }
 
-__device__ __forceinline__ void load_bias8(const LinearParams& p, long c, float (&b)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = p.bias != nullptr && c + i < p.N ? __ldg(p.bias + c + i) : 0.f;
+// f(std::integral_constant) for the descriptor's activation: one branch for a whole block of outputs.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  switch (act) {
+    case MOE_ACT_RELU: f(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+    case MOE_ACT_SILU: f(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+    case MOE_ACT_GELU: f(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+    case MOE_ACT_GELU_TANH: f(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, MOE_ACT_NONE>{});
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -286,7 +315,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       if (finish && c8 < p.N) {
         float b[8];
         load_bias8(p, c8, b);
-        finish8(p, col, c8, z, b);
+        const uint4 res = load_residual8(p, col, c8);
+        with_activation(p.act, [&](auto act) { finish8<decltype(act)::value>(p, col, c8, z, b, res); });
       }
       u = end;
     }
@@ -303,24 +333,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // rows, 32 KB for 64 elements of k, half of what two single CTAs load for the same products.  Persistent and
 // warp-specialised: warp 0 TMA, warp 1 MMA (even CTA), eight epilogue warps, two accumulators in TMEM so that
 // a tile's epilogue runs beside the next tile's MMAs.  The epilogue brings 32 x 32 blocks through shared
-// memory (pitch 33: both directions free of bank conflicts) so that a lane finishes eight consecutive
-// features of a row and stores 16 bytes.
+// memory (pitch 36: 16-byte accesses free of bank conflicts both ways) so that a lane finishes eight
+// consecutive features of a row and stores 16 bytes; what it reads (bias, residual) is loaded before the
+// block's accumulators are, since its latency, not its arithmetic, bounded the tile.
 //
-// splits > 1 (fewer tiles than SMs): K is cut, each unit leaves fp32 partials in the workspace and the last
-// CTA of a tile to arrive adds them in order and finishes; nobody waits.
+// splits > 1 (fewer tiles than SMs; single CTAs): K is cut over a cluster of 2, 4 or 8 CTAs.  Each leaves its
+// fp32 tile in shared memory, and each adds up and finishes its share of the columns from all of them
+// through distributed shared memory, in the order of the slices.
 // ------------------------------------------------------------------------------------------------
 constexpr int kGemmStagesMax = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kLinThreads = 64 + kEpiWarps * 32;
-constexpr int kEpiPitch = 33;
+constexpr int kEpiPitch = 36;
+constexpr int kSplitPitch = 132;   // floats per row of a cut tile in shared memory
 
 struct LinGemmSmem {
   uint64_t full[kGemmStagesMax], empty[kGemmStagesMax];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
-  int abort, last;
-  float stage[kEpiWarps][32 * kEpiPitch];
+  int abort;
+  alignas(16) float stage[kEpiWarps][32 * kEpiPitch];
 };
 
 template <bool kPair>
@@ -331,12 +364,6 @@ struct LinTile {
   static constexpr int kBBytes = kBN / kCtas * 128;
   static constexpr int kStage = kABytes + kBBytes;
 };
-
-__device__ __forceinline__ void epilogue_sync() {
-  __syncwarp();
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-static_assert(kEpiWarps * 32 == 256, "the named barrier's thread count");
 
 // Unit w: tile and slice of k.  Tiles run through groups of eight token blocks, all of a group's token blocks
 // for one feature block before the next, so that what runs at a time shares weights and tokens in L2.
@@ -505,13 +532,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   } else {
     // ---------------- epilogue ----------------
     const int q = warp & 3, part = (warp - 2) >> 2;   // TMEM lane quadrant; 32-column blocks part, part + 2, ...
-    const int eid = threadIdx.x - 64;
     float* stage = sm->stage[warp - 2];
     const uint32_t acc_empty_leader = kPair ? cluster_addr(&sm->acc_empty[0], 0) : 0u;   // + 8 * buffer
     int acc = 0;
     uint32_t acc_ph = 0;
     for (int w = first; w < units; w += step) {
       const LinUnit u = lin_unit(p, w);
+      const int row0 = (u.m * L::kCtas + (int)rank) * 128 + q * 32;   // the warp's first token
+      const long col0 = (long)u.n * L::kBN;
       uint32_t taddr = 0;
       auto await_acc = [&]() {
         const bool got = mbar_wait_warp(&sm->acc_full[acc], acc_ph, abort, p.ew, 514);
@@ -539,7 +567,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       };
       constexpr int kMine = L::kBN / 64;   // 32-column blocks of this warp
       float sum[kPromote ? kMine : 1][32];
-      // with cut tiles a CTA has one unit, and its warps meet at barriers below even after an abort
       bool have = await_acc();
       if constexpr (kPromote) {
         const int chunks = (u.k1 - u.k0 + kPromoteSteps - 1) / kPromoteSteps;
@@ -559,82 +586,95 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           release();
         }
       }
-      if (!have && p.splits == 1) break;
-      const int row0 = (u.m * L::kCtas + (int)rank) * 128 + q * 32;   // the warp's first token
-      const long col0 = (long)u.n * L::kBN;
-      // partials: [unit][CTA of the pair][column][128 rows]
-      constexpr int kPart = L::kBN * 128;
-      float* part_base = p.scratch + (((size_t)u.tile * p.splits) * L::kCtas + rank) * kPart + q * 32 + lane;
-      bool finish = true;
-      if (p.splits > 1) {
-        float* mine = part_base + (size_t)u.split * L::kCtas * kPart;
+      if (!have) break;
+      // block b of the warp's columns, as accumulated
+      auto block = [&](int b, float (&v)[32]) {
+        if constexpr (kPromote) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = sum[b][i];
+        } else {
+          load_block(part + 2 * b, v);
+        }
+      };
+      if (!kPair && p.splits > 1) {   // the stages are drained: the tile takes their place
+        float* dst = reinterpret_cast<float*>(smem) + (q * 32 + lane) * kSplitPitch;
 #pragma unroll
         for (int b = 0; b < kMine; ++b) {
-          if (!have) break;
-          const int blk = part + 2 * b;
           float v[32];
-          if constexpr (!kPromote) load_block(blk, v);
+          block(b, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) __stcg(mine + (blk * 32 + i) * 128, kPromote ? sum[kPromote ? b : 0][i] : v[i]);
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + (part + 2 * b) * 32 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
-        if (!kPromote) release();
-        __threadfence();
-        epilogue_sync();
-        if (eid == 0) {
-          int* done = &p.ew->linear_done[u.tile * L::kCtas + (int)rank];
-          const int last = atomicAdd(done, 1) == p.splits - 1;
-          if (last) *done = 0;
-          __threadfence();
-          sm->last = last;
-        }
-        epilogue_sync();
-        finish = sm->last != 0;
-        epilogue_sync();   // before the next unit's flag
+        break;   // one unit a CTA
       }
-      if (finish) {
-#pragma unroll
+      with_activation(p.act, [&](auto act) {
+#pragma unroll(kPromote ? kMine : 1)
         for (int b = 0; b < kMine; ++b) {
-          const int blk = part + 2 * b;
-          const long c = col0 + blk * 32;
+          const long c = col0 + (part + 2 * b) * 32, c8 = c + (lane & 3) * 8;
           if (row0 >= p.T || c >= p.N) break;   // warp-uniform: nothing of this block (or later ones) is kept
-          float v[32];
-          if (p.splits == 1) {
-            if constexpr (kPromote) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = sum[b][i];
-            } else {
-              load_block(blk, v);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            for (int s = 0; s < p.splits; ++s) {
-              const float* src = part_base + (size_t)s * L::kCtas * kPart + blk * 32 * 128;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += __ldcg(src + i * 128);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) stage[lane * kEpiPitch + i] = v[i];
-          __syncwarp();
-          const long c8 = c + (lane & 3) * 8;
+          const bool in = c8 < p.N;
           float b8[8];
+          uint4 res[4];
           load_bias8(p, c8, b8);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = (lane >> 2) + 8 * i;
-            if (row0 + r < p.T && c8 < p.N) {
-              float z[8];
+            const int t = row0 + (lane >> 2) + 8 * i;
+            res[i] = in && t < p.T ? load_residual8(p, t, c8) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          float v[32];
+          block(b, v);
+          if (!kPromote && b == kMine - 1) release();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) z[j] = stage[r * kEpiPitch + (lane & 3) * 8 + j];
-              finish8(p, row0 + r, c8, z, b8);
-            }
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(stage + lane * kEpiPitch + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            const float4* src = reinterpret_cast<const float4*>(stage + r * kEpiPitch + (lane & 3) * 8);
+            const float4 lo = src[0], hi = src[1];
+            const float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (in && row0 + r < p.T) finish8<decltype(act)::value>(p, row0 + r, c8, z, b8, res[i]);
           }
           __syncwarp();
         }
-      }
-      if (p.splits == 1 && !kPromote) release();
+      });
+      // blocks past T or N were not loaded: the accumulator is released here
+      if (!kPromote && (row0 >= p.T || col0 + (part + 2 * (kMine - 1)) * 32 >= p.N)) release();
     }
+  }
+
+  if (!kPair && p.splits > 1) {
+    __syncwarp();
+    cluster_sync();   // every slice's tile is in shared memory
+    if (warp >= 2) {
+      const LinUnit u = lin_unit(p, blockIdx.x);
+      const int width = L::kBN / p.splits, per_row = width / 8, rows = min(128, p.T - u.m * 128);
+      with_activation(p.act, [&](auto act) {
+        for (int i = (int)threadIdx.x - 64; i < rows * per_row; i += kEpiWarps * 32) {
+          const int r = i / per_row, c = u.split * width + (i - r * per_row) * 8;
+          const long c8 = (long)u.n * L::kBN + c;
+          if (c8 >= p.N) continue;
+          const int t = u.m * 128 + r;
+          float z[8] = {}, b8[8];
+          load_bias8(p, c8, b8);
+          const uint4 res = load_residual8(p, t, c8);
+          const float* mine = reinterpret_cast<const float*>(smem) + r * kSplitPitch + c;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            if (s >= p.splits) break;
+            const uint32_t src = cluster_addr(mine, s);
+            const float4 lo = ld_cluster_v4(src), hi = ld_cluster_v4(src + 16);
+            z[0] += lo.x; z[1] += lo.y; z[2] += lo.z; z[3] += lo.w;
+            z[4] += hi.x; z[5] += hi.y; z[6] += hi.z; z[7] += hi.w;
+          }
+          finish8<decltype(act)::value>(p, t, c8, z, b8, res);
+        }
+      });
+    }
+    __syncwarp();
+    cluster_sync();   // nobody reads this CTA's tile any more
   }
 
   tc_fence_before();
@@ -670,9 +710,10 @@ cudaError_t launch_gemm(const CUtensorMap& map_x, const CUtensorMap& map_w, Line
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   unsigned n = 0;
-  if (kPair) {
+  const int cluster = kPair ? 2 : p.splits;
+  if (cluster > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.x = cluster;
     attr[n].val.clusterDim.y = 1;
     attr[n].val.clusterDim.z = 1;
     ++n;
@@ -683,7 +724,7 @@ cudaError_t launch_gemm(const CUtensorMap& map_x, const CUtensorMap& map_w, Line
   if (kPair && cudaOccupancyMaxActiveClusters(&active, kernel, &cfg) == cudaSuccess && active > 0 && active < slots)
     slots = active;
   (void)cudaGetLastError();
-  cfg.gridDim = dim3(L::kCtas * std::min(units, slots));
+  cfg.gridDim = dim3(p.splits > 1 ? units : L::kCtas * std::min(units, slots));
   cfg.numAttrs = n + pdl_attr(attr + n);
   return cudaLaunchKernelEx(&cfg, kernel, map_x, map_w, p);
 }
@@ -718,10 +759,10 @@ LinearPlan linear_plan(int T, int K, int N, int num_sms) {
     const int rows = pair ? 256 : 128, cols = pair ? 256 : 128, slots = pair ? num_sms / 2 : num_sms;
     const long m = ((long)T + rows - 1) / rows, n = ((long)N + cols - 1) / cols;
     const double loads = pair ? 1.0 : 0.5 * (std::min(T, 128) / 128.0) + 0.5, mma = pair ? 1.0 : 0.5;
-    for (int s = 1; s <= 16 && s <= nk; ++s) {
+    for (int s = 1; s <= (pair ? 1 : 8) && s <= nk; s *= 2) {
       if (s > 1 && m * n * s > slots) break;   // K is cut only to fill the SMs once
       const long units = m * n * s, waves = (units + slots - 1) / slots;
-      const double unit = ((nk + s - 1) / s) * std::max(loads, mma) + (pair ? 12 : 8) + (s > 1 ? 4 + 2 * s : 0);
+      const double unit = ((nk + s - 1) / s) * std::max(loads, mma) + (pair ? 12 : 8) + (s > 1 ? 3 : 0);
       const double cost = waves * unit;
       if (best == 0 || cost < best) {
         best = cost;
@@ -730,7 +771,6 @@ LinearPlan linear_plan(int T, int K, int N, int num_sms) {
         plan.n_tiles = (int)n;
         plan.splits = s;
         plan.w_box = 128;
-        plan.scratch_floats = s > 1 ? (size_t)units * rows * cols : 0;
       }
     }
   }

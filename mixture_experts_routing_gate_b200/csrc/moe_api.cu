@@ -1171,6 +1171,7 @@ moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int
   p.ldx = ldx; p.ldy = ldy; p.ldr = ldr;
   p.y_vec = aligned16(y) && ldy % (d.out_fp32 ? 4 : 8) == 0;
   p.residual_vec = aligned16(residual) && ldr % 8 == 0;
+  p.bias_vec = aligned16(bias);
   p.x = reinterpret_cast<const __nv_bfloat16*>(x);
   p.bias = bias;
   p.residual = reinterpret_cast<const __nv_bfloat16*>(residual);
