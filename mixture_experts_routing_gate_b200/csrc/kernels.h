@@ -191,6 +191,7 @@ struct LinearParams {
   int y_vec, residual_vec, bias_vec;  // rows of y / residual, and bias, start on 16-byte boundaries
   int stages;                 // set by the launcher
   int m_tiles, n_tiles, splits;
+  int x_box;                  // rows of x per tile in shared memory
   int test_stall;
   long long ldx, ldy, ldr;    // elements
   const __nv_bfloat16* x;
@@ -201,11 +202,12 @@ struct LinearParams {
   ErrorWord* ew;
 };
 // How a projection of T tokens runs: as a weight stream, or in tiles of CTA pairs or of single CTAs, these with
-// K cut over a cluster of `splits`.  w_box: weight rows per box of its tensor map (64 elements of k wide).
+// K cut over a cluster of `splits`.  x_box, w_box: rows per box of the
+// tensor maps (64 elements of k wide).
 struct LinearPlan {
   enum Kind { kStream, kSolo, kPair } kind;
   int m_tiles, n_tiles, splits;
-  int w_box;
+  int x_box, w_box;
   size_t scratch_floats;
 };
 LinearPlan linear_plan(int T, int K, int N, int num_sms);

@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // ------------------------------------------------------------------------------------------------
 // more tokens: tiles on the tcgen05 tensor cores
 //
-// A CTA's tile is 128 tokens (the MMA's M, a TMEM lane each) by kBN features (its N).  kPair: clusters of two
-// CTAs share MMAs of M = 256 by kBN = 256 (cta_group::2): each loads its 128 tokens and half of the weight
+// A CTA's tile is 128 tokens (the MMA's M, a TMEM lane each) by kN = 64 or 128 features (its N).  kPair: clusters
+// of two CTAs share MMAs of M = 256 by kN = 256 (cta_group::2): each loads its 128 tokens and half of the weight
 // rows, 32 KB for 64 elements of k, half of what two single CTAs load for the same products.  Persistent and
 // warp-specialised: warp 0 TMA, warp 1 MMA (even CTA), eight epilogue warps, two accumulators in TMEM so that
 // a tile's epilogue runs beside the next tile's MMAs.  The epilogue brings 32 x 32 blocks through shared
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // fp32 tile in shared memory, and each adds up and finishes its share of the columns from all of them
 // through distributed shared memory, in the order of the slices.
 // ------------------------------------------------------------------------------------------------
-constexpr int kGemmStagesMax = 8;
+constexpr int kGemmStagesMax = 12;
 constexpr int kEpiWarps = 8;
 constexpr int kLinThreads = 64 + kEpiWarps * 32;
 constexpr int kEpiPitch = 36;
@@ -356,13 +356,11 @@ struct LinGemmSmem {
   alignas(16) float stage[kEpiWarps][32 * kEpiPitch];
 };
 
-template <bool kPair>
+template <bool kPair, int kN>
 struct LinTile {
-  static constexpr int kBN = kPair ? 256 : 128;
+  static constexpr int kBN = kN;
   static constexpr int kCtas = kPair ? 2 : 1;
-  static constexpr int kABytes = 128 * 128;
   static constexpr int kBBytes = kBN / kCtas * 128;
-  static constexpr int kStage = kABytes + kBBytes;
 };
 
 // Unit w: tile and slice of k.  Tiles run through groups of eight token blocks, all of a group's token blocks
@@ -388,14 +386,17 @@ __device__ __forceinline__ LinUnit lin_unit(const LinearParams& p, int w) {
 // kPromoteSteps * 64, alternating between the two accumulators, and the epilogue warps add the chunks in
 // registers, rounding to nearest.
 constexpr int kPromoteSteps = 8;
-template <bool kPair, bool kPromote>
+template <bool kPair, int kN, bool kPromote>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        const __grid_constant__ LinearParams p) {
-  using L = LinTile<kPair>;
+  using L = LinTile<kPair, kN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  auto* sm = reinterpret_cast<LinGemmSmem*>(smem + p.stages * L::kStage);
+  // Batches below 128 tokens load and stage only x_box rows of x: the MMA then reads the weights (or the next
+  // stage, or the barriers) as its other rows, whose accumulators are never read.
+  const int a_bytes = p.x_box * 128, stage_bytes = a_bytes + L::kBBytes;
+  auto* sm = reinterpret_cast<LinGemmSmem*>(smem + p.stages * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -451,14 +452,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             break;
           }
           last_par[st] = (int)ph;
-          uint8_t* sa = smem + st * L::kStage;
-          if (leader) mbar_arrive_expect_tx(&sm->full[st], L::kCtas * L::kStage);   // whole boxes: zeros outside
+          uint8_t* sa = smem + st * stage_bytes;
+          if (leader) mbar_arrive_expect_tx(&sm->full[st], L::kCtas * stage_bytes);   // whole boxes: zeros outside
           if (kPair) {
             tma_load_2d_pair(sa, &map_x, full_leader + 8u * st, kb * 64, row_x);
-            tma_load_2d_pair(sa + L::kABytes, &map_w, full_leader + 8u * st, kb * 64, row_w);
+            tma_load_2d_pair(sa + a_bytes, &map_w, full_leader + 8u * st, kb * 64, row_w);
           } else {
             tma_load_2d(sa, &map_x, &sm->full[st], kb * 64, row_x);
-            tma_load_2d(sa + L::kABytes, &map_w, &sm->full[st], kb * 64, row_w);
+            tma_load_2d(sa + a_bytes, &map_w, &sm->full[st], kb * 64, row_w);
           }
           if (++st == p.stages) {
             st = 0;
@@ -504,8 +505,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + st * L::kStage);
-          const uint64_t a = sdesc_kmajor_sw128(sa), b = sdesc_kmajor_sw128(sa + L::kABytes);
+          const uint32_t sa = smem_u32(smem + st * stage_bytes);
+          const uint64_t a = sdesc_kmajor_sw128(sa), b = sdesc_kmajor_sw128(sa + a_bytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t accumulate = !start || kk != 0;
@@ -693,13 +694,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-template <bool kPair, bool kPromote>
+template <bool kPair, int kN, bool kPromote>
 cudaError_t launch_gemm(const CUtensorMap& map_x, const CUtensorMap& map_w, LinearParams p, int num_sms,
                         cudaStream_t stream) {
-  using L = LinTile<kPair>;
-  auto kernel = linear_gemm_kernel<kPair, kPromote>;
-  p.stages = (int)std::min<size_t>(kGemmStagesMax, (227 * 1024 - 1024 - sizeof(LinGemmSmem)) / L::kStage);
-  const size_t smem = 1024 + p.stages * (size_t)L::kStage + sizeof(LinGemmSmem);
+  using L = LinTile<kPair, kN>;
+  auto kernel = linear_gemm_kernel<kPair, kN, kPromote>;
+  const size_t stage = (size_t)p.x_box * 128 + L::kBBytes;
+  p.stages = (int)std::min<size_t>(kGemmStagesMax, (227 * 1024 - 1024 - sizeof(LinGemmSmem)) / stage);
+  const size_t smem = 1024 + p.stages * stage + sizeof(LinGemmSmem);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const int units = p.m_tiles * p.n_tiles * p.splits;
@@ -750,27 +752,31 @@ LinearPlan linear_plan(int T, int K, int N, int num_sms) {
     plan.scratch_floats = (size_t)num_sms * 2 * kStreamRows * 16;
     return plan;
   }
-  // Time of a choice in units of 64 elements of k on one SM: a step costs the larger of its MMAs (one unit
-  // for 128 x 256 x 64 per SM) and its loads (32 KB a unit), a unit of work also its epilogue and pipeline
-  // fill.
+  // Time of a choice, in loads of 32 KB by every SM at once (about 0.48 us: L2 gives all SMs together some
+  // 10 TB/s, which bounds these tiles before the tensor cores do).  A step is 64 elements of k; a unit of
+  // work also has its pipeline's fill and its epilogue, a cut one the join.  A cluster of 4 or 8 CTAs needs
+  // that many free SMs in one GPC, so fewer of those fit at a time.
   const long nk = (K + 63) / 64;
   double best = 0;
-  for (int pair = 0; pair < 2; ++pair) {
-    const int rows = pair ? 256 : 128, cols = pair ? 256 : 128, slots = pair ? num_sms / 2 : num_sms;
+  for (int kind = 0; kind < 3; ++kind) {
+    const bool pair = kind == 2;
+    const int rows = pair ? 256 : 128, cols = pair ? 256 : kind == 1 ? 128 : 64;
     const long m = ((long)T + rows - 1) / rows, n = ((long)N + cols - 1) / cols;
-    const double loads = pair ? 1.0 : 0.5 * (std::min(T, 128) / 128.0) + 0.5, mma = pair ? 1.0 : 0.5;
+    const double step = pair ? 1.0 : std::max(0.25, (std::min(T, 128) + cols) / 256.0);
     for (int s = 1; s <= (pair ? 1 : 8) && s <= nk; s *= 2) {
-      if (s > 1 && m * n * s > slots) break;   // K is cut only to fill the SMs once
-      const long units = m * n * s, waves = (units + slots - 1) / slots;
-      const double unit = ((nk + s - 1) / s) * std::max(loads, mma) + (pair ? 12 : 8) + (s > 1 ? 3 : 0);
-      const double cost = waves * unit;
+      const long slots = pair ? num_sms / 2 : s <= 2 ? num_sms : s == 4 ? num_sms * 6 / 7 : num_sms * 3 / 4;
+      const long units = m * n * s;
+      if (s > 1 && units > slots) break;   // K is cut only to fill the SMs once
+      const double unit = ((nk + s - 1) / s) * step + (pair ? 12 : 8) + (s > 1 ? 3 : 0);
+      const double cost = ((units + slots - 1) / slots) * unit;
       if (best == 0 || cost < best) {
         best = cost;
         plan.kind = pair ? LinearPlan::kPair : LinearPlan::kSolo;
         plan.m_tiles = (int)m;
         plan.n_tiles = (int)n;
         plan.splits = s;
-        plan.w_box = 128;
+        plan.w_box = pair ? 128 : cols;
+        plan.x_box = pair || T > 64 ? 128 : T > 32 ? 64 : 32;
       }
     }
   }
@@ -782,13 +788,16 @@ cudaError_t launch_linear(const LinearPlan& plan, const CUtensorMap& map_x, cons
   p.m_tiles = plan.m_tiles;
   p.n_tiles = plan.n_tiles;
   p.splits = plan.splits;
+  p.x_box = plan.x_box;
   if (plan.kind == LinearPlan::kStream)
     return p.T <= 8 ? launch_stream<1>(map_w, p, num_sms, stream) : launch_stream<2>(map_w, p, num_sms, stream);
-  if (plan.kind == LinearPlan::kPair)
-    return p.out_fp32 ? launch_gemm<true, true>(map_x, map_w, p, num_sms, stream)
-                      : launch_gemm<true, false>(map_x, map_w, p, num_sms, stream);
-  return p.out_fp32 ? launch_gemm<false, true>(map_x, map_w, p, num_sms, stream)
-                    : launch_gemm<false, false>(map_x, map_w, p, num_sms, stream);
+  auto gemm = [&](auto promote) {
+    constexpr bool kPromote = decltype(promote)::value;
+    if (plan.kind == LinearPlan::kPair) return launch_gemm<true, 256, kPromote>(map_x, map_w, p, num_sms, stream);
+    return plan.w_box == 128 ? launch_gemm<false, 128, kPromote>(map_x, map_w, p, num_sms, stream)
+                             : launch_gemm<false, 64, kPromote>(map_x, map_w, p, num_sms, stream);
+  };
+  return p.out_fp32 ? gemm(std::true_type{}) : gemm(std::false_type{});
 }
 
 }  // namespace moe

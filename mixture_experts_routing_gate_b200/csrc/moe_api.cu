@@ -1180,7 +1180,7 @@ moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int
   p.ew = at<ErrorWord>(ws, 0);
   p.test_stall = test_stall_flag();
   CUtensorMap mx{}, mw;
-  if (plan.kind != moe::LinearPlan::kStream && !make_map_rows(&mx, x, T, K, ldx, 128)) return MOE_ERR_CUDA;
+  if (plan.kind != moe::LinearPlan::kStream && !make_map_rows(&mx, x, T, K, ldx, plan.x_box)) return MOE_ERR_CUDA;
   if (!make_map_rows(&mw, w, N, K, K, plan.w_box)) return MOE_ERR_CUDA;
   return cuda_status(moe::launch_linear(plan, mx, mw, p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
