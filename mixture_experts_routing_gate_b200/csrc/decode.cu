@@ -81,7 +81,9 @@ struct Stage {
   static constexpr int kSOff = 2 * kBlock;
   static constexpr int kBytes = kSOff + (kFp4 ? kRows * 16 : 0);
   static constexpr int kRedPitch = kRows + 4;              // floats per token column (bank = 8 t + g)
-  static constexpr int kRedBufs = kFp4 ? 1 : 2;
+  // exchange buffers: two let a tile's sums run beside the next tile; the four-bit tiles of 9 to 16 tokens
+  // leave room for one
+  static constexpr int red_bufs(int nt) { return kFp4 && nt == 2 ? 1 : 2; }
 };
 
 template <bool kFp4, int kNT>
@@ -90,7 +92,7 @@ struct DecodeSmem {
   uint64_t empty[kMaxStages];
   uint64_t routed;                  // the lists below are complete
   int abort, last;
-  int up_done;                      // up tiles whose h this CTA has written
+  int up_done;                      // warps that wrote their part of an up tile's h, over the tiles so far
   int n_act;                        // active experts, the shared one first
   int sel_e[kMaxS];
   float sel_w[kMaxS];
@@ -103,8 +105,12 @@ struct DecodeSmem {
   int off_of[kMaxE];                // first row of each active expert
   float bias[kMaxE], offset[kMaxE]; // the router's (zeros where there is none)
   float scores[kRouterWarps][kMaxE];
-  alignas(16) float red[Stage<kFp4>::kRedBufs][kConsumerWarps * 8 * kNT * Stage<kFp4>::kRedPitch];
+  alignas(16) float red[Stage<kFp4>::red_bufs(kNT)][kConsumerWarps * 8 * kNT * Stage<kFp4>::kRedPitch];
 };
+
+// The consumer warps that write h of an up tile with n tokens: a token a warp (MXFP4), or four.
+template <bool kFp4>
+__device__ __forceinline__ int up_writers(int n) { return kFp4 ? n : (n + 3) / 4; }
 
 // Barriers of whole warps: lanes that waited on their own rejoin first.
 __device__ __forceinline__ void consumer_sync() {
@@ -114,10 +120,6 @@ __device__ __forceinline__ void consumer_sync() {
 __device__ __forceinline__ void router_sync() {
   __syncwarp();
   asm volatile("bar.sync 2, 96;" ::: "memory");
-}
-__device__ __forceinline__ void writers_sync() {   // the first four consumer warps
-  __syncwarp();
-  asm volatile("bar.sync 3, 128;" ::: "memory");
 }
 static_assert(kConsumers == 512 && kRouters == 96, "the named barriers' thread counts");
 
@@ -630,15 +632,20 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     const long long t0 = clock64();
     int seen = 0;
     for (TileIter it(nb); it.a < sm->n_act;) {
+      // a tile's writers are all past the tile before it, so the count passes each tile's total in turn
       const int done = *(volatile int*)&sm->up_done;
-      if (done == seen) {
+      int tiles = 0;
+      for (; it.a < sm->n_act && done >= seen + up_writers<kFp4>(sm->act_n[it.a]); it.next()) {
+        if (tiles++ == 0) __threadfence();
+        seen += up_writers<kFp4>(sm->act_n[it.a]);
+        atomicAdd(&p.ew->decode_ready[it.a], 1);
+      }
+      if (tiles > 0) {
+        atomicAdd(&p.ew->decode_arrive[1], tiles);
+      } else {
         __nanosleep(100);
         if (*abort || clock64() - t0 > 2 * kWaitLimitCycles) break;
-        continue;
       }
-      __threadfence();
-      atomicAdd(&p.ew->decode_arrive[1], done - seen);
-      for (; seen < done; ++seen, it.next()) atomicAdd(&p.ew->decode_ready[it.a], 1);
     }
   }
 }
@@ -666,9 +673,11 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&v)[4]) {
       : "r"(w));
 }
 
-// Whether some of four block scales may lie outside [2, 252] (bytes below 2, or whose complement is below 3).
-__device__ __forceinline__ uint32_t scales_outside(uint32_t s) {
-  return (((s - 0x02020202u) & ~s) | ((~s - 0x03030303u) & s)) & 0x80808080u;
+// Bits 7 of the bytes of `bad` are set where one of four block scales lies outside [2, 252]: s + 3 is then below
+// 5 modulo 256 (a carry out of a byte comes from such a scale too; other bits are not defined).
+__device__ __forceinline__ void note_scales(uint32_t s, uint32_t& bad) {
+  const uint32_t t = s + 0x03030303u;
+  bad |= (t - 0x05050505u) & ~t;
 }
 // Those clamped and reported.
 __device__ __noinline__ uint32_t clamp_scales(uint32_t s4, ErrorWord* ew) {
@@ -712,9 +721,9 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, c
     for (int i = 0; i < S::kRowTiles; ++i) {
       const uint32_t at = stage + S::kSOff + ((kDown ? 16 : 8) * i + g) * 16 + w * 2;
       sc[i] = lds16(at) | (lds16(at + kHi * 16) << 16);
-      bad |= scales_outside(sc[i]);
+      note_scales(sc[i], bad);
     }
-    if (bad != 0u) {
+    if ((bad & 0x80808080u) != 0u) {
 #pragma unroll
       for (int i = 0; i < S::kRowTiles; ++i) sc[i] = clamp_scales(sc[i], ew);
     }
@@ -897,14 +906,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     if (kFp4) consumer_sync();   // x16 is written
 
-    int count = 0, buf = 0, tiles_up = 0;   // stages of the tiles so far (the groups take turns)
+    int count = 0, buf = 0;      // stages of the tiles so far (the groups take turns)
     RingPos pos;                 // and where the next one lies
     bool routed = false;
     const uint32_t ring_addr = smem_u32(ring);
     const int grp = warp >> 3, w8 = warp & 7, g = lane >> 2, t = lane & 3;
     const int nb1 = p.I / S::kUp, nb2 = p.d / S::kRows;
     auto run_phase = [&](auto down_tag, TileIter it) {
-      constexpr bool kDown = decltype(down_tag)::value;
+      constexpr bool kDown = decltype(down_tag)::value, kTwo = S::red_bufs(kNT) == 2;
       const int K = kDown ? p.I : p.d, ns = (K + S::kChunk - 1) / S::kChunk;
       const uint16_t* rows[kNT];               // the tile's token rows, bf16 or (MXFP4) f16, at this warp's part
       const float* scales[kFp4 ? kNT : 1][2];
@@ -1001,7 +1010,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           fetch((grp ^ count) & 1);
         }
         float* red = sm->red[buf];
-        if (S::kRedBufs == 2) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
+        if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
         put_partials<kFp4, kNT>(red, warp, lane, acc, n <= 8 ? 1 : 2);
         consumer_sync();
         if constexpr (kDown) {
@@ -1009,7 +1018,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const int c = i / S::kRows, r = i % S::kRows;
             p.out[(size_t)(r0 + c) * p.d + blk * S::kRows + r] = sum_partials<kFp4, kNT>(red, c, r);
           }
-          if (S::kRedBufs == 1) consumer_sync();
         } else {
           // feature f of token c: gate and value sums, eight rows apart in their row tile
           const int c = tid / S::kUp, f = tid % S::kUp;
@@ -1027,23 +1035,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
               if (lane == 0) p.h_scale[(size_t)(r0 + c) * (p.I / 32) + blk] = block_down(eb);
             }
-            consumer_sync();
-            if (tid == 0) {
-              __threadfence_block();
-              *(volatile int*)&sm->up_done = ++tiles_up;
-            }
-          } else {
-            if (in) {
-              const __nv_bfloat16 v = __float2bfloat16_rn(h);
-              p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
-            }
-            if (warp < 4) writers_sync();   // 16 tokens x 8 features: the first 128 threads wrote
-            if (tid == 0) {
-              __threadfence_block();
-              *(volatile int*)&sm->up_done = ++tiles_up;
-            }
+          } else if (in) {
+            const __nv_bfloat16 v = __float2bfloat16_rn(h);
+            p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
+          }
+          // the router warps report the tile once all its writers are here
+          if (warp < up_writers<kFp4>(n)) {
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) atomicAdd(&sm->up_done, 1);
           }
         }
+        if (!kTwo) consumer_sync();
       }
     };
     run_phase(std::false_type{}, TileIter(nb1));
