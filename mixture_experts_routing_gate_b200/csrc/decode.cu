@@ -6,21 +6,21 @@
 // What bounds it: the weights of the chosen experts, read once -- every weight meets one to sixteen tokens,
 // far below the flops per byte at which the tensor cores would matter.  So the kernel is a weight stream:
 //
-// * one CTA per SM, all resident at once (cooperative launch).  One producer warp keeps TMA copies of 8 KB in
-//   flight into a ring of 110 to 200 KB of shared memory, sixteen consumer warps compute.  At 44 bytes/ns per
-//   SM the ring holds about 4 us of the stream, more than the memory latency, so the stream does not stop
-//   between the phases.  (Copies of single rows, 1 KB, cost about 65 ns each whoever issues them and held
-//   the stream at 2 TB/s.)
-// * three router warps turn the logits into the lists of experts while the consumers work on the shared
+// * one CTA per SM, all resident at once (cooperative launch).  Two producer warps keep TMA copies of 8 KB in
+//   flight into two rings of together 110 to 190 KB of shared memory, two groups of eight consumer warps
+//   compute, each on tiles of its own.  At 44 bytes/ns per SM the rings hold about 4 us of the stream, more
+//   than the memory latency, so the stream does not stop between the phases.  (Copies of single rows, 1 KB,
+//   cost about 65 ns each whoever issues them and held the stream at 2 TB/s.)
+// * two router warps turn the logits into the lists of experts while the consumers work on the shared
 //   expert, whose weights need no routing: the selection's latency (it runs once, on code and data that are
 //   not cached) is hidden.
 // * the products run on mma.sync with the weight rows as the 16-row operand and the tokens as the 8 columns
 //   of one or two tiles, so each weight is read from shared memory once.  The reduction index is permuted
 //   alike for both operands (thread t of a quad holds 8 consecutive elements), so that a weight fragment is
 //   one conflict-free shared load from TMA's 128-byte swizzle and a token fragment one 16-byte load from
-//   global memory (L1 or L2; a stage ahead), whatever the token's row.  Eight warps split a stage along k,
-//   the two groups of eight take alternate stages; the accumulators of a tile are added through shared
-//   memory in warp order: nothing depends on scheduling.
+//   global memory (L1 or L2; a stage ahead), whatever the token's row.  The eight warps of a group split a
+//   stage along k; the accumulators of a tile are added through shared memory in warp order: nothing depends
+//   on scheduling.  (All sixteen on one tile, in alternate stages, met at barriers twice as often.)
 // * in the up projections rows 0-7 of an MMA are w1's and rows 8-15 w3's, so gate and value of a feature meet
 //   in one accumulator tile.  A CTA starts on down-projection tiles of an expert as soon as all of that
 //   expert's h is written (a counter per expert), with no barrier between the projections; CTAs that had one
@@ -50,12 +50,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kConsumerWarps = 16;   // two groups of eight taking alternate stages
-constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kRouterWarps = 3;
+constexpr int kGroups = 2, kGroupWarps = 8, kGroupThreads = kGroupWarps * 32;   // a group has a ring and tiles
+constexpr int kConsumerWarps = kGroups * kGroupWarps, kConsumers = kConsumerWarps * 32;
+constexpr int kRouterWarps = 2;
 constexpr int kRouters = kRouterWarps * 32;
-constexpr int kDecThreads = kConsumers + 32 + kRouters;
-constexpr int kMaxStages = 16;
+constexpr int kDecThreads = kConsumers + kGroups * 32 + kRouters;
+constexpr int kMaxStages = 8;        // of a ring
 constexpr int kMaxT = kDecodeMaxTokens;
 constexpr int kMaxS = kMaxT * kMaxRouteTopk;
 constexpr int kMaxAct = kMaxS + 1;  // active experts: the shared one and at most one per slot
@@ -88,11 +88,11 @@ struct Stage {
 
 template <bool kFp4, int kNT>
 struct DecodeSmem {
-  uint64_t full[kMaxStages];
-  uint64_t empty[kMaxStages];
+  uint64_t full[kGroups][kMaxStages];
+  uint64_t empty[kGroups][kMaxStages];
   uint64_t routed;                  // the lists below are complete
   int abort, last;
-  int up_done;                      // warps that wrote their part of an up tile's h, over the tiles so far
+  int up_done[kGroups];             // warps that wrote their part of an up tile's h, over the group's tiles so far
   int n_act;                        // active experts, the shared one first
   int sel_e[kMaxS];
   float sel_w[kMaxS];
@@ -105,12 +105,13 @@ struct DecodeSmem {
   int off_of[kMaxE];                // first row of each active expert
   float bias[kMaxE], offset[kMaxE]; // the router's (zeros where there is none)
   float scores[kRouterWarps][kMaxE];
-  alignas(16) float red[Stage<kFp4>::red_bufs(kNT)][kConsumerWarps * 8 * kNT * Stage<kFp4>::kRedPitch];
+  // exchange buffers of the groups; the router logits' exchange takes the first 16 * 8 kNT * kGatePitch floats
+  alignas(16) float red[kGroups][Stage<kFp4>::red_bufs(kNT)][kGroupWarps * 8 * kNT * Stage<kFp4>::kRedPitch];
 };
 
-// The consumer warps that write h of an up tile with n tokens: a token a warp (MXFP4), or four.
+// The warps of a group that write h of an up tile with n tokens: a token at a time (MXFP4), or four.
 template <bool kFp4>
-__device__ __forceinline__ int up_writers(int n) { return kFp4 ? n : (n + 3) / 4; }
+__device__ __forceinline__ int up_writers(int n) { return kFp4 ? min(n, kGroupWarps) : (n + 3) / 4; }
 
 // Barriers of whole warps: lanes that waited on their own rejoin first.
 __device__ __forceinline__ void consumer_sync() {
@@ -119,9 +120,13 @@ __device__ __forceinline__ void consumer_sync() {
 }
 __device__ __forceinline__ void router_sync() {
   __syncwarp();
-  asm volatile("bar.sync 2, 96;" ::: "memory");
+  asm volatile("bar.sync 2, 64;" ::: "memory");
 }
-static_assert(kConsumers == 512 && kRouters == 96, "the named barriers' thread counts");
+__device__ __forceinline__ void group_sync(int group) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
+}
+static_assert(kConsumers == 512 && kRouters == 64 && kGroupThreads == 256, "the named barriers' thread counts");
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
   int v;
@@ -203,19 +208,19 @@ struct RingPos {
   }
 };
 
-// The tiles of a CTA as (active expert, block of rows).  Up projections: every gridDim-th tile.  Down
-// projections (early > 0): the `early` first rounds are taken by the CTAs from `first` on alone, which had
-// one up tile less than the others; then every gridDim-th.
+// The tiles of a group as (active expert, block of rows); groups are numbered over the grid, `self` of `all`.  Up
+// projections: every all-th tile.  Down projections (early > 0): the `early` first rounds are taken by the
+// groups from `first` on alone, which had one up tile less than the others; then every all-th.
 struct TileIter {
-  int j, a, blk, nb, early, first;
-  __device__ explicit TileIter(int nb_) : nb(nb_), early(0), first(0) { set(blockIdx.x); }
-  __device__ TileIter(int nb_, int early_, int first_) : nb(nb_), early(early_), first(first_) {
-    if (early > 0 && (int)blockIdx.x >= first) {
-      set((int)blockIdx.x - first);
+  int j, a, blk, nb, self, all, early, first;
+  __device__ TileIter(int nb_, int self_, int all_, int early_ = 0, int first_ = 0)
+      : nb(nb_), self(self_), all(all_), early(early_), first(first_) {
+    if (early > 0 && self >= first) {
+      set(self - first);
     } else {
-      const int all = early * ((int)gridDim.x - first);
+      const int before = early * (all - first);
       early = 0;
-      set(all + (int)blockIdx.x);
+      set(before + self);
     }
   }
   __device__ void set(int j_) {
@@ -224,22 +229,22 @@ struct TileIter {
     blk = j - a * nb;
   }
   __device__ void next() {
-    const int few = (int)gridDim.x - first;
     if (early > 1) {
       --early;
-      set(j + few);
-    } else if (early == 1) {   // j = (early rounds - 1) * few + blockIdx - first
+      set(j + all - first);
+    } else if (early == 1) {   // j = (early rounds - 1) * (all - first) + self - first
       early = 0;
-      set(j + few + first);
+      set(j + all);
     } else {
-      set(j + (int)gridDim.x);
+      set(j + all);
     }
   }
 };
-// The down projections' iterator: CTAs of index >= n_tiles % grid had one up tile less, worth d / I down tiles.
-__device__ __forceinline__ TileIter down_tiles(const DecodeParams& p, int n_act, int nb_up, int nb_down) {
-  const int m = (int)((long)n_act * nb_up % (int)gridDim.x);
-  return TileIter(nb_down, m == 0 ? 0 : (p.d + p.I / 2) / p.I, m);
+// The down projections' iterator: groups of index >= (up tiles) % all had one up tile less, worth d / I down
+// tiles.
+__device__ __forceinline__ TileIter down_tiles(const DecodeParams& p, int n_act, int nb_up, int nb_down, int self, int all) {
+  const int m = (int)((long)n_act * nb_up % all);
+  return TileIter(nb_down, self, all, m == 0 ? 0 : (p.d + p.I / 2) / p.I, m);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -355,7 +360,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 // Lane l holds experts 128 q + 4 l + r as i = 4 q + r, ascending in i.
 template <int PL>
 __device__ __forceinline__ void select_experts(const DecodeParams& p, const float* bias, const float* offset, int* sel_e,
-                                               float* sel_w, float* scores, int t, int lane) {
+                                               float* sel_w, float* scores, int t, bool report, int lane) {
   auto expert = [&](int i) { return (i >> 2) * 128 + 4 * lane + (i & 3); };
   float sc[PL];
   uint32_t key[PL];
@@ -413,13 +418,13 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, const floa
   if (p.token_ids != nullptr) {
     int tok = p.token_ids[t];
     if (tok < 0 || tok >= p.vocab) {
-      if (blockIdx.x == 0 && lane == 0) record_error(p.ew, MOE_ERR_DEVICE, tok);
+      if (report && lane == 0) record_error(p.ew, MOE_ERR_DEVICE, tok);
       tok = tok < 0 ? 0 : p.vocab - 1;
     }
     if (lane < p.k) {
       my_e = p.tid2eid[(size_t)tok * p.k + lane];
       if (my_e < 0 || my_e >= p.E) {
-        if (blockIdx.x == 0) record_error(p.ew, MOE_ERR_DEVICE, my_e);
+        if (report) record_error(p.ew, MOE_ERR_DEVICE, my_e);
         my_e = my_e < 0 ? 0 : p.E - 1;
       }
     }
@@ -569,7 +574,7 @@ __device__ __forceinline__ void build_lists(const DecodeParams& p, Smem* sm, int
 
 // The router warps: selection and lists, then the CTA's reports of finished up tiles.
 //
-// A round trip to L2 takes about 2 us under the weight stream, so up to three tokens are selected by every CTA
+// A round trip to L2 takes about 2 us under the weight stream, so up to two tokens are selected by every CTA
 // for itself, one per warp, from the partial logits of the whole grid.  More tokens are dealt to the first
 // CTAs, one each, and their choices read back after one more counter: 16 tokens 6 a warp took 34 us.
 template <bool kFp4, typename Smem>
@@ -582,9 +587,10 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     sm->offset[e] = p.logit_offset != nullptr ? p.logit_offset[e] : 0.f;
   }
   router_sync();
+  const bool report = dealt || blockIdx.x == 0;   // bad ids: once, by the CTA that selects the token
   auto select = [&](int t) {
-    if (p.E <= 256) select_experts<8>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, lane);
-    else select_experts<16>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, lane);
+    if (p.E <= 256) select_experts<8>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, report, lane);
+    else select_experts<16>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, report, lane);
   };
   if (lane == 0) grid_wait(&p.ew->decode_arrive[0], (int)gridDim.x, abort, p.ew, 404);
   __syncwarp();
@@ -627,13 +633,13 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
   }
   // Reports of finished up tiles, kept off the consumers' path: a release at GPU scope waits for the writes
   // before it, 1 to 2 us under the stream.
-  if (rt == 0) {
+  if (lane == 0) {   // a router warp for each group
     const int nb = p.I / Stage<kFp4>::kUp;
     const long long t0 = clock64();
     int seen = 0;
-    for (TileIter it(nb); it.a < sm->n_act;) {
+    for (TileIter it(nb, (int)blockIdx.x * kGroups + rw, (int)gridDim.x * kGroups); it.a < sm->n_act;) {
       // a tile's writers are all past the tile before it, so the count passes each tile's total in turn
-      const int done = *(volatile int*)&sm->up_done;
+      const int done = *(volatile int*)&sm->up_done[rw];
       int tiles = 0;
       for (; it.a < sm->n_act && done >= seen + up_writers<kFp4>(sm->act_n[it.a]); it.next()) {
         if (tiles++ == 0) __threadfence();
@@ -649,6 +655,7 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     }
   }
 }
+static_assert(kRouterWarps == kGroups, "one reports for each group");
 
 // ------------------------------------------------------------------------------------------------
 // consumers: one stage into the warp's accumulators
@@ -780,18 +787,20 @@ template <bool kFp4, int kNT>
 __device__ __forceinline__ float sum_partials(const float* red, int col, int row) {
   float v = 0.f;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) v += red[(w * 8 * kNT + col) * Stage<kFp4>::kRedPitch + row];
+  for (int w = 0; w < kGroupWarps; ++w) v += red[(w * 8 * kNT + col) * Stage<kFp4>::kRedPitch + row];
   return v;
 }
 
 // ------------------------------------------------------------------------------------------------
-// the weight stream: TMA copies by lane 0 and, for MXFP4, the scales by cp.async of all 32 lanes (then the
+// a group's weight stream: TMA copies by lane 0 and, for MXFP4, the scales by cp.async of all 32 lanes (then the
 // full barriers count their 32 arrivals too)
 // ------------------------------------------------------------------------------------------------
 template <bool kFp4, typename Smem>
 __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap* map_w1, const CUtensorMap* map_w3,
-                                        const CUtensorMap* map_w2, Smem* sm, uint8_t* ring, int lane) {
+                                        const CUtensorMap* map_w2, Smem* sm, uint8_t* ring, int grp, int lane) {
   using S = Stage<kFp4>;
+  const int self = (int)blockIdx.x * kGroups + grp, all = (int)gridDim.x * kGroups;
+  uint64_t *full = sm->full[grp], *empty = sm->empty[grp];
   if (p.test_stall) return;
   volatile int* abort = &sm->abort;
   constexpr int kColElems = S::kChunk / S::kCols;
@@ -804,16 +813,16 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
     const CUtensorMap *m0 = down ? map_w2 : map_w1, *m1 = down ? map_w2 : map_w3;
     const int row1 = down ? row + S::kRows / 2 : row;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
-      uint64_t* bar = &sm->full[pos.slot];
+      uint64_t* bar = &full[pos.slot];
       uint8_t* dst = ring + pos.slot * S::kBytes;
       if (kFp4) {
-        if (!mbar_wait_warp(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
+        if (!mbar_wait_warp(&empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
         const uint8_t* s0 = down ? p.w2s : p.w1s;
         const uint8_t* s1 = down ? p.w2s : p.w3s;
         cp_async16(smem_u32(dst + S::kSOff + lane * 16), s0 + ((size_t)(row + lane) * K + k0) / 32);
         cp_async16(smem_u32(dst + S::kSOff + (32 + lane) * 16), s1 + ((size_t)(row1 + lane) * K + k0) / 32);
         cp_async_arrive(bar);
-      } else if (!mbar_wait(&sm->empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) {
+      } else if (!mbar_wait(&empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) {
         return false;
       }
       if (lane == 0) {
@@ -827,7 +836,7 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
     return true;
   };
   const int nb1 = p.I / S::kUp, nb2 = p.d / S::kRows;
-  for (TileIter it(nb1); ok; it.next()) {
+  for (TileIter it(nb1, self, all); ok; it.next()) {
     if (it.a > 0 && !routed) {
       ok = kFp4 ? mbar_wait_warp(&sm->routed, 0, abort, p.ew, 403) : mbar_wait(&sm->routed, 0, abort, p.ew, 403);
       routed = true;
@@ -837,11 +846,11 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
     ok = tile(false, it.a == 0 ? p.E : sm->act_e[it.a], it.blk);
   }
   if (ok)
-    for (TileIter it = down_tiles(p, sm->n_act, nb1, nb2); ok && it.a < sm->n_act; it.next())
+    for (TileIter it = down_tiles(p, sm->n_act, nb1, nb2, self, all); ok && it.a < sm->n_act; it.next())
       ok = tile(true, it.a == 0 ? p.E : sm->act_e[it.a], it.blk);
   if (!ok) {   // let every copy already issued land before the CTA leaves
     for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-      mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+      mbar_wait(&full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
   }
 }
 
@@ -857,17 +866,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   using Smem = DecodeSmem<kFp4, kNT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Smem* sm = reinterpret_cast<Smem*>(ring + p.stages * S::kBytes);
+  Smem* sm = reinterpret_cast<Smem*>(ring + kGroups * p.stages * S::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  if (tid < p.stages) {
-    mbar_init(&sm->full[tid], kFp4 ? 1 + 32 : 1);
-    mbar_init(&sm->empty[tid], 8);
+  if (tid < kGroups * p.stages) {
+    mbar_init(&sm->full[tid / p.stages][tid % p.stages], kFp4 ? 1 + 32 : 1);
+    mbar_init(&sm->empty[tid / p.stages][tid % p.stages], kGroupWarps);
     fence_barrier_init();
   }
   if (tid == kConsumers) {
     mbar_init(&sm->routed, 1);
     sm->abort = 0;
-    sm->up_done = 0;
+    for (int i = 0; i < kGroups; ++i) sm->up_done[i] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_w1);
     tma_prefetch_desc(&map_w3);
@@ -892,12 +901,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // memory (all indices stay in range), so that they keep meeting at the same barriers.
   volatile int* abort = &sm->abort;
   const int G = (int)gridDim.x;
-  if (warp == kConsumerWarps) {
-    if (kFp4 || lane == 0) produce<kFp4>(p, &map_w1, &map_w3, &map_w2, sm, ring, lane);
-  } else if (warp > kConsumerWarps) {
-    route<kFp4>(p, sm, warp - kConsumerWarps - 1, lane);
+  if (warp >= kConsumerWarps && warp < kConsumerWarps + kGroups) {
+    const int grp = warp - kConsumerWarps;
+    if (kFp4 || lane == 0) produce<kFp4>(p, &map_w1, &map_w3, &map_w2, sm, ring + grp * p.stages * S::kBytes, grp, lane);
+  } else if (warp >= kConsumerWarps + kGroups) {
+    route<kFp4>(p, sm, warp - kConsumerWarps - kGroups, lane);
   } else {
-    gate_partials<kNT>(p, sm->red[0], warp, lane);
+    gate_partials<kNT>(p, sm->red[0][0], warp, lane);
     if (kFp4) scale_tokens(p, tid);
     consumer_sync();
     if (tid == 0) {
@@ -906,11 +916,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     if (kFp4) consumer_sync();   // x16 is written
 
-    int count = 0, buf = 0;      // stages of the tiles so far (the groups take turns)
-    RingPos pos;                 // and where the next one lies
+    RingPos pos;                 // the next stage
+    int buf = 0;
     bool routed = false;
-    const uint32_t ring_addr = smem_u32(ring);
-    const int grp = warp >> 3, w8 = warp & 7, g = lane >> 2, t = lane & 3;
+    const int grp = warp >> 3, w8 = warp & 7, g = lane >> 2, t = lane & 3, gtid = tid & (kGroupThreads - 1);
+    const int self = (int)blockIdx.x * kGroups + grp, all = G * kGroups;
+    const uint32_t ring_addr = smem_u32(ring + grp * p.stages * S::kBytes);
+    uint64_t *full = sm->full[grp], *empty = sm->empty[grp];
     const int nb1 = p.I / S::kUp, nb2 = p.d / S::kRows;
     auto run_phase = [&](auto down_tag, TileIter it) {
       constexpr bool kDown = decltype(down_tag)::value, kTwo = S::red_bufs(kNT) == 2;
@@ -980,77 +992,70 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       bool more = live();
       if (more) {
         enter();
-        fetch((grp ^ count) & 1);
+        fetch(0);
       }
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
-        RingPos mine = pos;
-        int s = (grp ^ count) & 1;
-        if (s) mine.step(1, p.stages);
-        for (; s < ns; s += 2, mine.step(2, p.stages)) {
+        for (int s = 0; s < ns; ++s, pos.step(1, p.stages)) {
           const TokenFrags<kFp4, kNT> cur = nxt;
-          if (kEarly && s + 2 < ns) fetch(s + 2);
-          stage_wait(&sm->full[mine.slot], mine.phase, abort, p.ew, kDown ? 406 : 405);
+          if (kEarly && s + 1 < ns) fetch(s + 1);
+          stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
-            const uint32_t stage = ring_addr + mine.slot * S::kBytes;
+            const uint32_t stage = ring_addr + pos.slot * S::kBytes;
             if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(stage, w8, lane, cur, acc, p.ew);
             else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, cur, acc, p.ew);
           }
-          if (!kEarly && s + 2 < ns) fetch(s + 2);
-          mbar_arrive_after_reads(&sm->empty[mine.slot]);
+          if (!kEarly && s + 1 < ns) fetch(s + 1);
+          mbar_arrive_after_reads(&empty[pos.slot]);
         }
-        count += ns;
-        pos.step(ns, p.stages);
         // the next tile's first fragments are under way while this one is added up
         it.next();
         more = live();
         if (more) {
           enter();
-          fetch((grp ^ count) & 1);
+          fetch(0);
         }
-        float* red = sm->red[buf];
+        float* red = sm->red[grp][buf];
         if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
-        put_partials<kFp4, kNT>(red, warp, lane, acc, n <= 8 ? 1 : 2);
-        consumer_sync();
+        put_partials<kFp4, kNT>(red, w8, lane, acc, n <= 8 ? 1 : 2);
+        group_sync(grp);
         if constexpr (kDown) {
-          for (int i = tid; i < n * S::kRows; i += kConsumers) {
+          for (int i = gtid; i < n * S::kRows; i += kGroupThreads) {
             const int c = i / S::kRows, r = i % S::kRows;
             p.out[(size_t)(r0 + c) * p.d + blk * S::kRows + r] = sum_partials<kFp4, kNT>(red, c, r);
           }
         } else {
           // feature f of token c: gate and value sums, eight rows apart in their row tile
-          const int c = tid / S::kUp, f = tid % S::kUp;
-          const bool in = c < n;
-          float h = 0.f;
-          if (in) {
+          const int f = gtid % S::kUp;
+          for (int c = gtid / S::kUp; c < n; c += kGroupThreads / S::kUp) {
             const int r = (f >> 3) * 16 + (f & 7);
             const float w = p.weight_in_expert && a > 0 ? sm->row_w[r0 + c] : 1.f;
-            h = swiglu(sum_partials<kFp4, kNT>(red, c, r), sum_partials<kFp4, kNT>(red, c, r + 8), p.swiglu_limit, w);
-          }
-          if constexpr (kFp4) {   // a warp holds one token's block of 32: its scale, then f16
-            const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu) >> 23);
-            if (in) {
+            const float h =
+                swiglu(sum_partials<kFp4, kNT>(red, c, r), sum_partials<kFp4, kNT>(red, c, r + 8), p.swiglu_limit, w);
+            uint16_t* dst = p.h + (size_t)(r0 + c) * p.I + blk * S::kUp + f;
+            if constexpr (kFp4) {   // a warp holds one token's block of 32: its scale, then f16
+              const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu) >> 23);
               const __half v = __float2half_rn(h * block_up(eb));
-              p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
+              *dst = *reinterpret_cast<const uint16_t*>(&v);
               if (lane == 0) p.h_scale[(size_t)(r0 + c) * (p.I / 32) + blk] = block_down(eb);
+            } else {
+              const __nv_bfloat16 v = __float2bfloat16_rn(h);
+              *dst = *reinterpret_cast<const uint16_t*>(&v);
             }
-          } else if (in) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(h);
-            p.h[(size_t)(r0 + c) * p.I + blk * S::kUp + f] = *reinterpret_cast<const uint16_t*>(&v);
           }
           // the router warps report the tile once all its writers are here
-          if (warp < up_writers<kFp4>(n)) {
+          if (w8 < up_writers<kFp4>(n)) {
             __threadfence_block();
             __syncwarp();
-            if (lane == 0) atomicAdd(&sm->up_done, 1);
+            if (lane == 0) atomicAdd(&sm->up_done[grp], 1);
           }
         }
-        if (!kTwo) consumer_sync();
+        if (!kTwo) group_sync(grp);
       }
     };
-    run_phase(std::false_type{}, TileIter(nb1));
-    run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2));
+    run_phase(std::false_type{}, TileIter(nb1, self, all));
+    run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
     consumer_sync();
     if (tid == 0) {
       red_release_add(&p.ew->decode_arrive[2], 1);
@@ -1109,11 +1114,7 @@ cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, co
   const size_t stage = fp4 ? Stage<true>::kBytes : Stage<false>::kBytes;
   const size_t fixed = fp4 ? (p.T <= 8 ? sizeof(DecodeSmem<true, 1>) : sizeof(DecodeSmem<true, 2>))
                            : (p.T <= 8 ? sizeof(DecodeSmem<false, 1>) : sizeof(DecodeSmem<false, 2>));
-  // An even number: a slot then always belongs to the same group of consumer warps, which waits for each of
-  // its fills in turn.  With an odd one the groups would share a slot, and the group of its second fill,
-  // running ahead inside a long tile, would take a first fill that has not landed for its own (a barrier's
-  // parity tells two successive phases apart, not three).
-  p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - fixed) / stage) & ~1;
+  p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - fixed) / stage / kGroups);   // of each group's ring
   auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1> : layer_decode_kernel<true, 2>)
                     : (p.T <= 8 ? layer_decode_kernel<false, 1> : layer_decode_kernel<false, 2>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

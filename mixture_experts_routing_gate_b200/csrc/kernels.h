@@ -153,7 +153,7 @@ struct DecodeParams {
   int weight_in_expert;       // routed rows of h carry their weights, the combine adds unweighted rows
   int vocab;                  // > 0 with token_ids and tid2eid: the token-id table routes
   int gate_splits;            // slices of k of the router logits
-  int stages;                 // of the weight ring (set by the launcher)
+  int stages;                 // of a weight ring (set by the launcher)
   int test_stall;             // failure-detection test hook: the producers issue no loads
   const int32_t* token_ids;   // [T] or null
   const int32_t* tid2eid;     // [vocab, k]

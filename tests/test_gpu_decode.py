@@ -224,6 +224,25 @@ def test_decode_flags_bad_ids_and_scales(M):
     _check(M, cfg, li, w4, y, w, idx, cnt, ws)
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 16])
+def test_decode_flags_the_bad_id_of_any_token(M, T):
+    cfg = TINY.replace(T=T, n_groups=1, n_limited_groups=1, topk=2, bias_std=None)
+    li, _ = _layer(cfg)
+    table = torch.tensor([[0, 3], [9, 1]], dtype=torch.int32, device="cuda")
+    ws = M.Workspace(M.layer_desc(cfg), T)
+    for t in range(T):
+        ids = torch.ones(T, dtype=torch.int32, device="cuda")
+        ids[t] = 1000 + t
+        idx = _decode(M, cfg, li, None, ws, table, ids)[2]
+        assert M.moe_get_error(ws) == (M.MOE_ERR_DEVICE, 1000 + t)
+        assert idx.tolist() == [[9, 1]] * T      # clamped to the last row
+    bad = torch.tensor([[0, 3], [16, -1]], dtype=torch.int32, device="cuda")
+    idx = _decode(M, cfg, li, None, ws, bad, torch.ones(T, dtype=torch.int32, device="cuda"))[2]
+    st, info = M.moe_get_error(ws)
+    assert st == M.MOE_ERR_DEVICE and info in (16, -1)
+    assert idx.tolist() == [[15, 0]] * T
+
+
 def test_decode_not_a_number_stays_in_its_token(M):
     cfg = TINY.replace(T=5)
     li, _ = _layer(cfg)
