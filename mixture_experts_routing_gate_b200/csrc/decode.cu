@@ -90,7 +90,7 @@ template <bool kFp4, int kNT>
 struct DecodeSmem {
   uint64_t full[kGroups][kMaxStages];
   uint64_t empty[kGroups][kMaxStages];
-  uint64_t routed;                  // the lists below are complete
+  uint64_t routed, weighted;        // the lists below are complete; the slots' weights are too
   int abort, last;
   int up_done[kGroups];             // warps that wrote their part of an up tile's h, over the group's tiles so far
   int n_act;                        // active experts, the shared one first
@@ -345,11 +345,12 @@ __device__ __forceinline__ void scale_tokens(const DecodeParams& p, int tid) {
 // ------------------------------------------------------------------------------------------------
 // phase 2: selection, one warp per token
 // ------------------------------------------------------------------------------------------------
-// Affinity with the accurate exponential and division: the selection compares these values.
-__device__ __forceinline__ float affinity_rn(float l, int score_func) {
-  if (score_func == MOE_SCORE_SQRT_SOFTPLUS) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
-  return __fdiv_rn(1.f, 1.f + expf(-l));
+// Affinities with the accurate exponential and division: the selection compares these values.  The affinity
+// of -inf is 0 in both, so lanes need no bounds and their experts' chains of instructions interleave.
+__device__ __forceinline__ float affinity_softplus(float l) {
+  return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
 }
+__device__ __forceinline__ float affinity_sigmoid(float l) { return __fdiv_rn(1.f, 1.f + expf(-l)); }
 
 // An unsigned key that orders as the float does; never 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -407,10 +408,12 @@ __device__ __forceinline__ void select_experts(const DecodeParams& p, const floa
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 #pragma unroll
     for (int i = 0; i < PL; ++i) sc[i] = __fdiv_rn(sc[i], z);
+  } else if (p.score_func == MOE_SCORE_SQRT_SOFTPLUS) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) sc[i] = affinity_softplus(sc[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (expert(i) < p.E) sc[i] = affinity_rn(sc[i], p.score_func);
+    for (int i = 0; i < PL; ++i) sc[i] = affinity_sigmoid(sc[i]);
   }
 
   int my_e = 0;          // lane j holds slot j's expert and unbiased score
@@ -592,6 +595,19 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     if (p.E <= 256) select_experts<8>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, report, lane);
     else select_experts<16>(p, sm->bias, sm->offset, sm->sel_e, sm->sel_w, sm->scores[rw], t, report, lane);
   };
+  // The table names a hash-routed token's experts before there are logits: their weights are then needed by
+  // the combine alone (unless h carries them).
+  const bool early = p.token_ids != nullptr && !p.weight_in_expert;
+  if (early) {
+    for (int s = rt; s < S; s += kRouters) {
+      const int tok = min(max(p.token_ids[s / p.k], 0), p.vocab - 1);   // bad ids are reported by the selection below
+      sm->sel_e[s] = min(max(p.tid2eid[(size_t)tok * p.k + s % p.k], 0), p.E - 1);
+      sm->sel_w[s] = 0.f;
+    }
+    router_sync();
+    build_lists(p, sm, rt, lane);
+    if (rt == 0) mbar_arrive(&sm->routed);
+  }
   if (lane == 0) grid_wait(&p.ew->decode_arrive[0], (int)gridDim.x, abort, p.ew, 404);
   __syncwarp();
   if (!dealt) {
@@ -617,8 +633,11 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     }
   }
   router_sync();
-  build_lists(p, sm, rt, lane);
-  if (rt == 0) mbar_arrive(&sm->routed);
+  if (!early) {
+    build_lists(p, sm, rt, lane);
+    if (rt == 0) mbar_arrive(&sm->routed);
+  }
+  if (rt == 0) mbar_arrive(&sm->weighted);
   if (blockIdx.x == 0) {
     for (int s = rt; s < S; s += kRouters) {
       if (p.weights_out != nullptr) p.weights_out[s] = sm->sel_w[s];
@@ -875,6 +894,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   if (tid == kConsumers) {
     mbar_init(&sm->routed, 1);
+    mbar_init(&sm->weighted, 1);
     sm->abort = 0;
     for (int i = 0; i < kGroups; ++i) sm->up_done[i] = 0;
     fence_barrier_init();
@@ -1061,6 +1081,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       red_release_add(&p.ew->decode_arrive[2], 1);
       grid_wait(&p.ew->decode_arrive[2], G, abort, p.ew, 407);
     }
+    stage_wait(&sm->weighted, 0, abort, p.ew, 411);
     consumer_sync();
 
     // ---------------- combine, slot order then the shared expert ----------------
