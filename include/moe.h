@@ -108,8 +108,8 @@ typedef struct {
 /* Bytes of workspace needed by any entry point below for a batch of T tokens. */
 size_t moe_workspace_bytes(const moe_layer_desc* desc, int T);
 
-/* Clears the workspace's control words (the error word and dispatch's block counter, which every
- * call leaves at zero).  Call once after allocating a workspace, before any other call uses it
+/* Clears the workspace's control words (the error word, dispatch's block counter and the serving calls'
+ * grid counters, which every call leaves at zero).  Call once after allocating a workspace, before any other call uses it
  * (asynchronous). */
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
 
@@ -321,6 +321,7 @@ moe_status moe_forward(const moe_layer_desc* desc, int T, const moe_bf16* x, con
  * resident and streams the chosen experts' weights without a break from the gate to the combine.
  * Values: the same formulas with fp32 accumulation; h is rounded once to bf16 and, unlike
  * moe_forward, the expert outputs stay in fp32 until the combine.  Results do not depend on scheduling.
+ * As in moe_forward, a hash-routed call uses neither bias nor logit_offset.
  * The selection may differ from moe_forward's where two experts' scores agree to fp32 rounding.
  * A table row that names an expert twice counts it twice (in the weights, in y and in counts_out).
  * desc->options, token_chunk and gate_prepared choose nothing here (they are still checked).
@@ -401,8 +402,9 @@ moe_status moe_forward_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* 
 
 /*
  * moe_decode with MXFP4 expert weights (as for moe_expert_ffn_mxfp4: dim % 512 == 0, inter_dim % 512
- * == 0).  The weights are used exactly and the activations in bf16 -- the values of
- * MOE_OPT_MXFP4_BF16_ACTIVATIONS, whether the option is set or not.
+ * == 0).  The weights are used exactly.  The activations keep the precision of bf16 whether
+ * MOE_OPT_MXFP4_BF16_ACTIVATIONS is set or not: x and h are held in f16 in blocks of 32 elements with a
+ * power-of-two scale each, exact for values of x down to 2^-32 of their block's largest, h rounded once (2^-12).
  */
 moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x,
                             const int32_t* token_ids, const int32_t* tid2eid, int vocab,

@@ -19,17 +19,13 @@
 namespace moe {
 
 // ------------------------------------------------------------------------------------------------
-// control words (first 4096 bytes of every workspace)
+// error word (first 256 bytes of every workspace)
 // ------------------------------------------------------------------------------------------------
 struct ErrorWord {
   int status;           // 0 or the first moe_status recorded
   int info;             // the offending value (index, token id, or a wait site)
   int dispatch_ticket;  // dispatch's count of finished histogram blocks (0 between calls)
-  int decode_arrive[4]; // the one-launch layer's grid counters: logits, up tiles, down, tokens (0 between calls)
-  int decode_done;      //   and CTAs finished
-  int decode_ready[144];  // its up tiles finished, per active expert (0 between calls)
-  int linear_done[512];   // the linear projection's parts of a tile finished (0 between calls)
-  int pad[360];
+  int pad[61];
 };
 
 __device__ __forceinline__ void record_error(ErrorWord* ew, int status, int info) {
@@ -75,15 +71,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// A warp's arrival after it has read a shared-memory stage with plain loads, which frees the stage for the
-// next TMA copy.  Every lane's reads are fenced first: without the fence a weight-stream kernel read rows of
-// the next fill (seen as wrong rows in about one launch of six, in the stage behind a tile's end).
-__device__ __forceinline__ void mbar_arrive_after_reads(uint64_t* bar) {
-  __threadfence_block();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
@@ -220,16 +207,6 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_u32(smem_dst)),
       "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// The 3-D box at (c0 = innermost, c1, c2), as tma_load_2d.
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                            int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -386,13 +363,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 // Generic-proxy shared-memory writes of this thread become visible to the async proxy (TMA, MMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// 16-byte load from the shared memory of a CTA of the cluster (address from cluster_addr).
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
 }
 
 // 16-byte store into the shared memory of a CTA of the cluster (address from cluster_addr).

@@ -26,7 +26,9 @@
 //   expert's h is written (a counter per expert), with no barrier between the projections; CTAs that had one
 //   up tile less take more of the first down tiles.
 //
-// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16.
+// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16.  Measured (floor at
+// the measured copy bandwidth in brackets): d = 7168, I = 2048, 9 experts, one token 132 us (122); d = 5120,
+// I = 1536, 16 tokens on 384 unevenly popular experts 344 us (278); d = 256, one token 18 us.
 //
 // MXFP4 weights: what travels is a quarter, so the arithmetic of decoding is what has to be cheap.  The
 // hardware's E2M1 -> f16 conversion takes 73 codes/clock/SM (measured; the stream brings 44), where placing
@@ -35,7 +37,9 @@
 // 2^15 and held in f16 (exact for bf16 values down to 2^-32 of the block's largest, off by 2^-40 of it
 // below), and the block's scale and the weights' UE8M0 scale multiply the fp32 accumulators of its 32
 // elements.  An up tile is 32 features, one block of h, whose scale its epilogue can therefore choose; tiles
-// are 64 rows, 512 codes of k a stage, so a token fragment serves four MMA row tiles.
+// are 64 rows, 512 codes of k a stage, so a token fragment serves four MMA row tiles.  Measured: d = 7168, I =
+// 2048, one token 74 us (33), eight tokens 350 us (206); half of the issue slots are used, so what is left is in
+// the consumers' instructions and waits.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -43,8 +47,8 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "serving.h"
+#include "stream.cuh"
 
 namespace moe {
 
@@ -63,7 +67,7 @@ constexpr int kMaxE = 512;
 constexpr int kGateRows = 16;       // router rows per unit of the logit phase
 constexpr int kGatePitch = 20;      // floats per token column of its exchange (bank = 8 t + g)
 static_assert(kMaxT <= 16, "two column tiles of eight tokens, token masks of 16 bits");
-static_assert(kMaxAct <= sizeof(ErrorWord::decode_ready) / sizeof(int), "a counter for every active expert");
+static_assert(kMaxAct <= sizeof(GridCounters::ready) / sizeof(int), "a counter for every active expert");
 
 // A stage holds kChunk elements of k of kRows weight rows as two blocks (up: w1's and w3's rows), each as TMA
 // writes a box of 128 bytes x kRows / 2 x kCols in the 128-byte swizzle -- the 16-byte unit u of row r of
@@ -608,7 +612,7 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     build_lists(p, sm, rt, lane);
     if (rt == 0) mbar_arrive(&sm->routed);
   }
-  if (lane == 0) grid_wait(&p.ew->decode_arrive[0], (int)gridDim.x, abort, p.ew, 404);
+  if (lane == 0) grid_wait(&p.gc->arrive[0], (int)gridDim.x, abort, p.ew, 404);
   __syncwarp();
   if (!dealt) {
     for (int t = rw; t < p.T; t += kRouterWarps) select(t);
@@ -622,10 +626,10 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
         p.route_w[t * p.k + lane] = sm->sel_w[t * p.k + lane];
       }
       __syncwarp();
-      if (lane == 0) red_release_add(&p.ew->decode_arrive[3], 1);
+      if (lane == 0) red_release_add(&p.gc->arrive[3], 1);
     }
     router_sync();
-    if (lane == 0) grid_wait(&p.ew->decode_arrive[3], p.T, abort, p.ew, 410);
+    if (lane == 0) grid_wait(&p.gc->arrive[3], p.T, abort, p.ew, 410);
     __syncwarp();
     for (int s = rt; s < S; s += kRouters) {
       sm->sel_e[s] = *abort ? 0 : __ldcg(p.route_e + s);   // after an abort the scratch may hold anything
@@ -663,10 +667,10 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
       for (; it.a < sm->n_act && done >= seen + up_writers<kFp4>(sm->act_n[it.a]); it.next()) {
         if (tiles++ == 0) __threadfence();
         seen += up_writers<kFp4>(sm->act_n[it.a]);
-        atomicAdd(&p.ew->decode_ready[it.a], 1);
+        atomicAdd(&p.gc->ready[it.a], 1);
       }
       if (tiles > 0) {
-        atomicAdd(&p.ew->decode_arrive[1], tiles);
+        atomicAdd(&p.gc->arrive[1], tiles);
       } else {
         __nanosleep(100);
         if (*abort || clock64() - t0 > 2 * kWaitLimitCycles) break;
@@ -931,8 +935,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (kFp4) scale_tokens(p, tid);
     consumer_sync();
     if (tid == 0) {
-      red_release_add(&p.ew->decode_arrive[0], 1);
-      if (kFp4) grid_wait(&p.ew->decode_arrive[0], G, abort, p.ew, 408);
+      red_release_add(&p.gc->arrive[0], 1);
+      if (kFp4) grid_wait(&p.gc->arrive[0], G, abort, p.ew, 408);
     }
     if (kFp4) consumer_sync();   // x16 is written
 
@@ -964,8 +968,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (!all_ready && it.a != ready_a) {   // all of this expert's h is written?
           int done = 0;
           if (lane == 0) {
-            done = ld_acquire(&p.ew->decode_arrive[1]) >= sm->n_act * nb1;
-            if (!done) grid_wait(&p.ew->decode_ready[it.a], nb1, abort, p.ew, 402);
+            done = ld_acquire(&p.gc->arrive[1]) >= sm->n_act * nb1;
+            if (!done) grid_wait(&p.gc->ready[it.a], nb1, abort, p.ew, 402);
           }
           all_ready = __shfl_sync(0xffffffffu, done, 0) != 0;
           ready_a = it.a;
@@ -1078,8 +1082,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
     consumer_sync();
     if (tid == 0) {
-      red_release_add(&p.ew->decode_arrive[2], 1);
-      grid_wait(&p.ew->decode_arrive[2], G, abort, p.ew, 407);
+      red_release_add(&p.gc->arrive[2], 1);
+      grid_wait(&p.gc->arrive[2], G, abort, p.ew, 407);
     }
     stage_wait(&sm->weighted, 0, abort, p.ew, 411);
     consumer_sync();
@@ -1112,12 +1116,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // the last CTA to get here leaves the grid's counters at zero (nobody waits on them any more)
   __syncwarp();
   __syncthreads();
-  if (tid == 0) sm->last = atomicAdd(&p.ew->decode_done, 1) == G - 1;
+  if (tid == 0) sm->last = atomicAdd(&p.gc->done, 1) == G - 1;
   __syncthreads();
   if (sm->last) {
-    if (tid < kMaxAct) p.ew->decode_ready[tid] = 0;
-    if (tid < 4) p.ew->decode_arrive[tid] = 0;
-    if (tid == 4) p.ew->decode_done = 0;
+    if (tid < kMaxAct) p.gc->ready[tid] = 0;
+    if (tid < 4) p.gc->arrive[tid] = 0;
+    if (tid == 4) p.gc->done = 0;
   }
 }
 

@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "serving.h"
 
 namespace moe {
 
@@ -34,6 +35,7 @@ using moe::ErrorWord;
 
 constexpr size_t kAlign = 1024;
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
+static_assert(sizeof(ErrorWord) == moe::kErrorBytes, "the control words follow the error word");
 constexpr size_t kPreparedHeader = 1024;   // prepared router weight: flag word, then the three planes
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -97,7 +99,7 @@ WsLayout ws_layout(const moe_layer_desc& d, int T) {
     o = align_up(o + bytes);
     return at;
   };
-  L.err = take(sizeof(ErrorWord));
+  L.err = take(moe::kControlBytes);
   L.flag = take(sizeof(int));
   L.planes = take(3 * E * D * 2);
   L.indices = take(S * 4);
@@ -908,6 +910,7 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.weights_out = weights_out; p.indices_out = indices_out; p.counts_out = counts_out;
   p.ew = at<ErrorWord>(ws, L.err);
+  p.gc = at<moe::GridCounters>(ws, L.err + moe::kErrorBytes);
   CUtensorMap m1, m3, m2;
   const uint64_t n = d.n_experts + 1, per = fp4 != nullptr ? 1 : 4;   // bytes of two weights
   const uint32_t rows = fp4 != nullptr ? 32 : 8, cols = fp4 != nullptr ? 2 : 8;
@@ -929,7 +932,7 @@ moe_status check_linear(const moe_linear_desc* d, int T) {
 // The linear projection's workspace: the control words, then the partials of cut tiles.
 size_t linear_ws_bytes(const moe_linear_desc& d, int T) {
   const moe::LinearPlan plan = moe::linear_plan(T, d.in_features, d.out_features, num_sms());
-  return align_up(sizeof(ErrorWord)) + align_up(plan.scratch_floats * sizeof(float));
+  return align_up(moe::kControlBytes) + align_up(plan.scratch_floats * sizeof(float));
 }
 
 }  // namespace
@@ -945,8 +948,8 @@ size_t moe_workspace_bytes(const moe_layer_desc* desc, int T) {
 }
 
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
-  if (ws == nullptr || ws_bytes < sizeof(ErrorWord)) return MOE_ERR_WORKSPACE;
-  return cuda_status(cudaMemsetAsync(ws, 0, sizeof(ErrorWord), reinterpret_cast<cudaStream_t>(stream)));
+  if (ws == nullptr || ws_bytes < moe::kControlBytes) return MOE_ERR_WORKSPACE;
+  return cuda_status(cudaMemsetAsync(ws, 0, moe::kControlBytes, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_gate_prepared_bytes(const moe_layer_desc* desc) {
@@ -1164,7 +1167,7 @@ moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_WORKSPACE;
   const int sms = num_sms();
   const moe::LinearPlan plan = moe::linear_plan(T, K, N, sms);
-  if (ws_bytes < align_up(sizeof(ErrorWord)) + align_up(plan.scratch_floats * sizeof(float))) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < align_up(moe::kControlBytes) + align_up(plan.scratch_floats * sizeof(float))) return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;
   moe::LinearParams p{};
   p.T = T; p.K = K; p.N = N; p.act = d.activation; p.out_fp32 = d.out_fp32;
@@ -1176,8 +1179,9 @@ moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int
   p.bias = bias;
   p.residual = reinterpret_cast<const __nv_bfloat16*>(residual);
   p.y = y;
-  p.scratch = at<float>(ws, align_up(sizeof(ErrorWord)));
+  p.scratch = at<float>(ws, align_up(moe::kControlBytes));
   p.ew = at<ErrorWord>(ws, 0);
+  p.gc = at<moe::GridCounters>(ws, moe::kErrorBytes);
   p.test_stall = test_stall_flag();
   CUtensorMap mx{}, mw;
   if (plan.kind != moe::LinearPlan::kStream && !make_map_rows(&mx, x, T, K, ldx, plan.x_box)) return MOE_ERR_CUDA;

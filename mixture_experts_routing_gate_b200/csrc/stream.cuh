@@ -1,0 +1,34 @@
+// Device-side building blocks of the serving kernels, beside those of common.cuh.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// The 3-D box at (c0 = innermost, c1, c2), as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 16-byte load from the shared memory of a CTA of the cluster (address from cluster_addr).
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// A warp's arrival after it has read a shared-memory stage with plain loads, which frees the stage for the
+// next TMA copy.  Every lane's reads are fenced first: without the fence a weight-stream kernel read rows of
+// the next fill (seen as wrong rows in about one launch of six, in the stage behind a tile's end).
+__device__ __forceinline__ void mbar_arrive_after_reads(uint64_t* bar) {
+  __threadfence_block();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+}  // namespace moe
