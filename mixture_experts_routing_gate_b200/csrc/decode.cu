@@ -953,7 +953,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int K = kDown ? p.I : p.d, ns = (K + S::kChunk - 1) / S::kChunk;
       const uint16_t* rows[kNT];               // the tile's token rows, bf16 or (MXFP4) f16, at this warp's part
       const float* scales[kFp4 ? kNT : 1][2];
-      TokenFrags<kFp4, kNT> nxt;
+      // Fragments of the next kSets stages, each set loaded again as soon as its stage is done.  Two where the
+      // registers hold them: an L2 round trip under the stream is longer than a stage.
+      constexpr int kSets = kFp4 ? 1 : 2;
+      TokenFrags<kFp4, kNT> frags[kSets];
       int ready_a = -1;
       bool all_ready = !kDown;
       // Whether the iterator stands on a tile (waits for the lists at the first routed one).
@@ -990,7 +993,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
       };
-      auto fetch = [&](int s) {   // the fragments of stage s of the tile entered (zeros past its end)
+      auto fetch = [&](int s, TokenFrags<kFp4, kNT>& nxt) {   // those of stage s of the tile entered (zeros past its end)
         const bool in = s * S::kChunk + w8 * 64 < K;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
@@ -1010,35 +1013,37 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
       };
-      // the next stage's fragments are loaded before this one's products where the registers hold both
-      // (bf16 with one column tile: 3 % faster), behind them elsewhere (no spills: 6 % faster)
-      constexpr bool kEarly = !kFp4 && kNT == 1;
       bool more = live();
       if (more) {
         enter();
-        fetch(0);
+#pragma unroll
+        for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
       }
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
-        for (int s = 0; s < ns; ++s, pos.step(1, p.stages)) {
-          const TokenFrags<kFp4, kNT> cur = nxt;
-          if (kEarly && s + 1 < ns) fetch(s + 1);
+        auto one_stage = [&](int s, TokenFrags<kFp4, kNT>& tok) {
           stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
             const uint32_t stage = ring_addr + pos.slot * S::kBytes;
-            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(stage, w8, lane, cur, acc, p.ew);
-            else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, cur, acc, p.ew);
+            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(stage, w8, lane, tok, acc, p.ew);
+            else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, tok, acc, p.ew);
           }
-          if (!kEarly && s + 1 < ns) fetch(s + 1);
+          if (s + kSets < ns) fetch(s + kSets, tok);
           mbar_arrive_after_reads(&empty[pos.slot]);
+          pos.step(1, p.stages);
+        };
+        for (int s = 0; s < ns; s += kSets) {
+          one_stage(s, frags[0]);
+          if (kSets == 2 && s + 1 < ns) one_stage(s + 1, frags[kSets - 1]);
         }
         // the next tile's first fragments are under way while this one is added up
         it.next();
         more = live();
         if (more) {
           enter();
-          fetch(0);
+#pragma unroll
+          for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
         }
         float* red = sm->red[grp][buf];
         if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
