@@ -26,9 +26,10 @@
 //   expert's h is written (a counter per expert), with no barrier between the projections; CTAs that had one
 //   up tile less take more of the first down tiles.
 //
-// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16.  Measured (floor at
+// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16, or held in two bf16
+// parts where that costs nothing (small layers; see the launcher).  Measured (floor at
 // the measured copy bandwidth in brackets): d = 7168, I = 2048, 9 experts, one token 132 us (122); d = 5120,
-// I = 1536, 16 tokens on 384 unevenly popular experts 344 us (278); d = 256, one token 18 us.
+// I = 1536, 16 tokens on 384 unevenly popular experts 327 to 377 us (278); d = 256, one token 18 us.
 //
 // MXFP4 weights: what travels is a quarter, so the arithmetic of decoding is what has to be cheap.  The
 // hardware's E2M1 -> f16 conversion takes 73 codes/clock/SM (measured; the stream brings 44), where placing
@@ -685,9 +686,10 @@ static_assert(kRouterWarps == kGroups, "one reports for each group");
 // ------------------------------------------------------------------------------------------------
 // The warp's 64 elements of a stage's token rows (rows g and g + 8 of the tile's): two blocks of 32, of which
 // thread t holds 8 elements each; MXFP4: and the blocks' scales of the token columns 2t, 2t + 1 (+ 8).
-template <bool kFp4, int kNT>
+// bf16 h (kLo): and the second parts of its elements.
+template <bool kFp4, int kNT, bool kLo>
 struct TokenFrags {
-  uint4 v[kNT][2];
+  uint4 v[kNT][2], lo[kLo ? kNT : 1][2];
   float2 scale[kFp4 ? kNT : 1][2];   // .x, .y: the two blocks; of columns 2t and 2t + 1
 };
 
@@ -724,8 +726,8 @@ __device__ __noinline__ uint32_t clamp_scales(uint32_t s4, ErrorWord* ew) {
 }
 
 // w: the warp's place in its group of eight, which takes elements [64 w, 64 w + 64) of the stage.
-template <bool kFp4, bool kDown, int NT, int kNT>
-__device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT>& tok,
+template <bool kFp4, bool kDown, int NT, int kNT, bool kLo>
+__device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT, kLo>& tok,
                                               float (&acc)[Stage<kFp4>::kRowTiles][kNT][4], ErrorWord* ew) {
   using S = Stage<kFp4>;
   const int g = lane >> 2, t = lane & 3;
@@ -740,6 +742,11 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, c
         const uint4 b = tok.v[nt][kb];
         mma_16816<false>(acc[0][nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
         mma_16816<false>(acc[0][nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        if constexpr (kLo) {
+          const uint4 r = tok.lo[nt][kb];
+          mma_16816<false>(acc[0][nt], lo.x, hi.x, lo.y, hi.y, r.x, r.y);
+          mma_16816<false>(acc[0][nt], lo.z, hi.z, lo.w, hi.w, r.z, r.w);
+        }
       }
     }
   } else {
@@ -881,7 +888,8 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
 // the kernel
 // ------------------------------------------------------------------------------------------------
 // kNT: column tiles of eight tokens (1 for batches of at most 8, whose fragments then take half the registers).
-template <bool kFp4, int kNT>
+// kTwoParts: h in two bf16 parts (bf16 experts).
+template <bool kFp4, int kNT, bool kTwoParts>
 __global__ void __launch_bounds__(kDecThreads, 1)
     layer_decode_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w3,
                         const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ DecodeParams p) {
@@ -955,8 +963,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const float* scales[kFp4 ? kNT : 1][2];
       // Fragments of the next kSets stages, each set loaded again as soon as its stage is done.  Two where the
       // registers hold them: an L2 round trip under the stream is longer than a stage.
-      constexpr int kSets = kFp4 ? 1 : 2;
-      TokenFrags<kFp4, kNT> frags[kSets];
+      constexpr bool kLo = kDown && kTwoParts;
+      constexpr int kSets = kFp4 || (kLo && kNT == 2) ? 1 : 2;
+      TokenFrags<kFp4, kNT, kLo> frags[kSets];
       int ready_a = -1;
       bool all_ready = !kDown;
       // Whether the iterator stands on a tile (waits for the lists at the first routed one).
@@ -993,16 +1002,22 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
       };
-      auto fetch = [&](int s, TokenFrags<kFp4, kNT>& nxt) {   // those of stage s of the tile entered (zeros past its end)
+      auto fetch = [&](int s, TokenFrags<kFp4, kNT, kLo>& nxt) {   // those of stage s of the tile entered (zeros past its end)
         const bool in = s * S::kChunk + w8 * 64 < K;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
           nxt.v[nt][0] = nxt.v[nt][1] = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (kLo) nxt.lo[nt][0] = nxt.lo[nt][1] = make_uint4(0u, 0u, 0u, 0u);
           if (in && rows[nt] != nullptr) {
             const uint4* at = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk);
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)   // written during this kernel, except x itself: read from L2
               nxt.v[nt][kb] = kDown || kFp4 ? __ldcg(at + kb * 4) : __ldg(at + kb * 4);
+            if constexpr (kLo) {
+              const uint4* lo = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk + p.h_lo);
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb) nxt.lo[nt][kb] = __ldcg(lo + kb * 4);
+            }
           }
           if constexpr (kFp4) {
 #pragma unroll
@@ -1022,12 +1037,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
-        auto one_stage = [&](int s, TokenFrags<kFp4, kNT>& tok) {
+        auto one_stage = [&](int s, TokenFrags<kFp4, kNT, kLo>& tok) {
           stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
             const uint32_t stage = ring_addr + pos.slot * S::kBytes;
-            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1>(stage, w8, lane, tok, acc, p.ew);
-            else consume_stage<kFp4, kDown, kNT>(stage, w8, lane, tok, acc, p.ew);
+            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
+            else consume_stage<kFp4, kDown, kNT, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
           }
           if (s + kSets < ns) fetch(s + kSets, tok);
           mbar_arrive_after_reads(&empty[pos.slot]);
@@ -1071,6 +1086,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             } else {
               const __nv_bfloat16 v = __float2bfloat16_rn(h);
               *dst = *reinterpret_cast<const uint16_t*>(&v);
+              if constexpr (kTwoParts) {
+                const float rest = h - __bfloat162float(v);   // NaN for an infinite h, whose first part says enough
+                const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+                dst[p.h_lo] = *reinterpret_cast<const uint16_t*>(&lo);
+              }
             }
           }
           // the router warps report the tile once all its writers are here
@@ -1145,8 +1165,14 @@ cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, co
   const size_t fixed = fp4 ? (p.T <= 8 ? sizeof(DecodeSmem<true, 1>) : sizeof(DecodeSmem<true, 2>))
                            : (p.T <= 8 ? sizeof(DecodeSmem<false, 1>) : sizeof(DecodeSmem<false, 2>));
   p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - fixed) / stage / kGroups);   // of each group's ring
-  auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1> : layer_decode_kernel<true, 2>)
-                    : (p.T <= 8 ? layer_decode_kernel<false, 1> : layer_decode_kernel<false, 2>);
+  // h rounded once to bf16, as everywhere in the library, puts about 0.7 of y's own rounding on top of it.  A
+  // second bf16 part (16 bits together) takes that away for a second MMA and fragment in the down projection:
+  // 142 us instead of 136 on the V3-shaped layer (T = 1), but nothing on small layers, which are bound by latency
+  // (18.4 us both ways at d = 256), so those take it: up to 32 MB of weights, 5 us of the stream.
+  const bool two = (long)(std::min(p.T * p.k, p.E) + 1) * p.d * p.I * 6 <= (32l << 20);
+  auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1, false> : layer_decode_kernel<true, 2, false>)
+                : two ? (p.T <= 8 ? layer_decode_kernel<false, 1, true> : layer_decode_kernel<false, 2, true>)
+                      : (p.T <= 8 ? layer_decode_kernel<false, 1, false> : layer_decode_kernel<false, 2, false>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // no more CTAs than any phase has work for: small layers pay for each arrival at the barriers

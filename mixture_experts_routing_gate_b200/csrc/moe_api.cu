@@ -83,7 +83,7 @@ namespace {
 // first, the scales 1 KiB-aligned after them) and the quantised x in a region of its own.
 struct WsLayout {
   size_t err, flag, planes, indices, weights, counts, offsets, row_of_slot, tok_of_row, w_perm, hist, base,
-      chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, dec_x16, dec_x_scale, dec_h_scale, total;
+      chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, dec_x16, dec_x_scale, dec_h_scale, dec_h, total;
   size_t xp_scales, h_scales, xq_scales;   // offsets of the scales inside x_perm, h and xq
 };
 
@@ -127,6 +127,7 @@ WsLayout ws_layout(const moe_layer_desc& d, int T) {
   L.dec_out = take(dec ? (S + T) * D * 4 : 0);
   L.dec_x16 = take(dec ? (size_t)T * D * 2 : 0);
   L.dec_x_scale = take(dec ? (size_t)T * (D / 32) * 4 : 0);
+  L.dec_h = take(dec ? 2 * (S + T) * I * 2 : 0);
   L.dec_h_scale = take(dec ? (S + T) * (I / 32) * 4 : 0);
   L.total = o;
   return L;
@@ -904,7 +905,8 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   p.route_w = at<float>(ws, L.weights);
   p.x16 = at<uint16_t>(ws, L.dec_x16);
   p.x_scale = at<float>(ws, L.dec_x_scale);
-  p.h = at<uint16_t>(ws, L.h);
+  p.h = at<uint16_t>(ws, L.dec_h);
+  p.h_lo = (long long)(T + T * d.topk) * d.inter_dim;
   p.h_scale = at<float>(ws, L.dec_h_scale);
   p.out = at<float>(ws, L.dec_out);
   p.y = reinterpret_cast<__nv_bfloat16*>(y);

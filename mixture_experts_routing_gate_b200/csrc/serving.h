@@ -39,6 +39,7 @@ struct DecodeParams {
   uint16_t* x16;              // MXFP4: [T, d] scratch, x in f16 blocks of 32, and
   float* x_scale;             //   their scales [T, d / 32]
   uint16_t* h;                // [T + T * k, I] scratch (bf16; MXFP4: f16 blocks): shared rows first, then the experts'
+  long long h_lo;             // bf16: elements from h to its second parts (h = first + second, 16 bits)
   float* h_scale;             // MXFP4: [T + T * k, I / 32] scratch
   int32_t* route_e;           // [T * k] scratch: the selection, handed round the grid
   float* route_w;             // [T * k]
