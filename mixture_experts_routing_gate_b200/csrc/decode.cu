@@ -98,6 +98,7 @@ struct DecodeSmem {
   uint64_t routed, weighted;        // the lists below are complete; the slots' weights are too
   int abort, last;
   int up_done[kGroups];             // warps that wrote their part of an up tile's h, over the group's tiles so far
+  int issued[kGroups];              // stages whose copies a group's producer has started
   int n_act;                        // active experts, the shared one first
   int sel_e[kMaxS];
   float sel_w[kMaxS];
@@ -131,6 +132,20 @@ __device__ __forceinline__ void group_sync(int group) {
   __syncwarp();
   asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
 }
+// group_sync that tells every warp of the group whether one of them says so.
+__device__ __forceinline__ bool group_any(int group, bool v) {
+  int any;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 256, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(3 + group), "r"((int)v)
+      : "memory");
+  return any != 0;
+}
 static_assert(kConsumers == 512 && kRouters == 64 && kGroupThreads == 256, "the named barriers' thread counts");
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
@@ -148,6 +163,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Waits until `*counter` reaches `target`.  Bounded as mbar_wait is.
 __device__ __forceinline__ bool grid_wait(const int* counter, int target, volatile int* abort, ErrorWord* ew, int site) {
@@ -165,13 +181,14 @@ __device__ __forceinline__ bool grid_wait(const int* counter, int target, volati
   }
 }
 
-// A consumer's wait for a stage: the usual, successful test inline; after an abort no waiting at all.
-__device__ __noinline__ void stage_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
-  if (!*abort) mbar_wait(bar, parity, abort, ew, site);
+// A consumer warp's wait: the usual, successful test inline; after an abort no waiting at all.  False, in every
+// lane alike, where a lane's wait was given up.
+__device__ __noinline__ bool stage_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  return !*abort && mbar_wait(bar, parity, abort, ew, site);
 }
-__device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
-  if (!mbar_try_wait(bar, parity)) stage_wait_slow(bar, parity, abort, ew, site);
-  __syncwarp();
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  const bool got = mbar_try_wait(bar, parity) || stage_wait_slow(bar, parity, abort, ew, site);
+  return __all_sync(0xffffffffu, got);
 }
 
 template <bool kF16>
@@ -587,6 +604,7 @@ __device__ __forceinline__ void build_lists(const DecodeParams& p, Smem* sm, int
 // CTAs, one each, and their choices read back after one more counter: 16 tokens 6 a warp took 34 us.
 template <bool kFp4, typename Smem>
 __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, int lane) {
+  if (p.test_stall == kStallRouter) return;
   volatile int* abort = &sm->abort;
   const int rt = rw * 32 + lane, S = p.T * p.k;
   const bool dealt = p.T > kRouterWarps && (int)gridDim.x >= p.T;
@@ -831,9 +849,10 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
   using S = Stage<kFp4>;
   const int self = (int)blockIdx.x * kGroups + grp, all = (int)gridDim.x * kGroups;
   uint64_t *full = sm->full[grp], *empty = sm->empty[grp];
-  if (p.test_stall) return;
+  if (p.test_stall == kStallCopies) return;
   volatile int* abort = &sm->abort;
   constexpr int kColElems = S::kChunk / S::kCols;
+  const int most = p.test_stall == kStallLater || (p.test_stall == kStallOneCta && blockIdx.x == 0) ? 5 : 0x7fffffff;
   RingPos pos;
   int issued = 0;
   bool ok = true, routed = false;
@@ -843,6 +862,7 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
     const CUtensorMap *m0 = down ? map_w2 : map_w1, *m1 = down ? map_w2 : map_w3;
     const int row1 = down ? row + S::kRows / 2 : row;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
+      if (issued == most) return false;
       uint64_t* bar = &full[pos.slot];
       uint8_t* dst = ring + pos.slot * S::kBytes;
       if (kFp4) {
@@ -878,10 +898,19 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
   if (ok)
     for (TileIter it = down_tiles(p, sm->n_act, nb1, nb2, self, all); ok && it.a < sm->n_act; it.next())
       ok = tile(true, it.a == 0 ? p.E : sm->act_e[it.a], it.blk);
-  if (!ok) {   // let every copy already issued land before the CTA leaves
-    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-      mbar_wait(&full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+  if (lane == 0) sm->issued[grp] = issued;
+}
+
+// After an abort: every copy that the group's producer warp has started lands before the CTA leaves.
+template <typename Smem>
+__device__ __forceinline__ void drain(Smem* sm, int stages, int grp, int lane) {
+  cp_async_wait_all();
+  if (lane == 0) {
+    const int issued = sm->issued[grp];
+    for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+      mbar_wait(&sm->full[grp][i % stages], (i / stages) & 1, nullptr, nullptr, 0, 200000000LL);
   }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -908,7 +937,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     mbar_init(&sm->routed, 1);
     mbar_init(&sm->weighted, 1);
     sm->abort = 0;
-    for (int i = 0; i < kGroups; ++i) sm->up_done[i] = 0;
+    sm->n_act = 1;
+    for (int i = 0; i < kGroups; ++i) sm->up_done[i] = sm->issued[i] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_w1);
     tma_prefetch_desc(&map_w3);
@@ -929,8 +959,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   __syncthreads();
 
-  // Every wait below is bounded; after one has run out the threads go on over whatever lies in shared
-  // memory (all indices stay in range), so that they keep meeting at the same barriers.
+  // Every wait below is bounded.  A consumer warp whose wait was given up touches nothing any more: it neither
+  // reads the lists (which may not exist) nor frees a stage (whose fill may be under way: a second fill would
+  // arm its barrier twice).  It goes on to the next barrier of its group and says so there, and the whole group
+  // leaves the tiles at that barrier.  The combine is left out, and the producers see their copies land.
   volatile int* abort = &sm->abort;
   const int G = (int)gridDim.x;
   if (warp >= kConsumerWarps && warp < kConsumerWarps + kGroups) {
@@ -969,21 +1001,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       int ready_a = -1;
       bool all_ready = !kDown;
       // Whether the iterator stands on a tile (waits for the lists at the first routed one).
+      bool lost = false;   // a wait of this warp was given up
       auto live = [&]() {
         if (it.a > 0 && !routed) {
-          stage_wait(&sm->routed, 0, abort, p.ew, 409);
-          routed = true;
+          routed = stage_wait(&sm->routed, 0, abort, p.ew, 409);
+          lost |= !routed;
         }
-        return it.a == 0 || it.a < sm->n_act;
+        return it.a == 0 || (routed && it.a < sm->n_act);
       };
       auto enter = [&]() {
         if (!all_ready && it.a != ready_a) {   // all of this expert's h is written?
-          int done = 0;
+          int done = 0;   // 1: of this expert, 2: of all
           if (lane == 0) {
-            done = ld_acquire(&p.gc->arrive[1]) >= sm->n_act * nb1;
-            if (!done) grid_wait(&p.gc->ready[it.a], nb1, abort, p.ew, 402);
+            if (ld_acquire(&p.gc->arrive[1]) >= sm->n_act * nb1) done = 2;
+            else done = grid_wait(&p.gc->ready[it.a], nb1, abort, p.ew, 402);
           }
-          all_ready = __shfl_sync(0xffffffffu, done, 0) != 0;
+          done = __shfl_sync(0xffffffffu, done, 0);
+          all_ready = done == 2;
+          lost |= done == 0;
           ready_a = it.a;
         }
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a];
@@ -1034,11 +1069,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
       }
+      if (group_any(grp, lost)) return false;
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
         auto one_stage = [&](int s, TokenFrags<kFp4, kNT, kLo>& tok) {
-          stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
+          lost = lost || !stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
+          if (lost) return;
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
             const uint32_t stage = ring_addr + pos.slot * S::kBytes;
             if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
@@ -1054,7 +1091,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         // the next tile's first fragments are under way while this one is added up
         it.next();
-        more = live();
+        more = !lost && live();
         if (more) {
           enter();
 #pragma unroll
@@ -1063,7 +1100,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         float* red = sm->red[grp][buf];
         if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
         put_partials<kFp4, kNT>(red, w8, lane, acc, n <= 8 ? 1 : 2);
-        group_sync(grp);
+        if (group_any(grp, lost)) return false;
         if constexpr (kDown) {
           for (int i = gtid; i < n * S::kRows; i += kGroupThreads) {
             const int c = i / S::kRows, r = i % S::kRows;
@@ -1102,20 +1139,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         if (!kTwo) group_sync(grp);
       }
+      return true;
     };
-    run_phase(std::false_type{}, TileIter(nb1, self, all));
-    run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
+    if (run_phase(std::false_type{}, TileIter(nb1, self, all)))
+      run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
     consumer_sync();
-    if (tid == 0) {
+    if (tid == 0) {   // after an abort too: the other CTAs are not kept waiting
       red_release_add(&p.gc->arrive[2], 1);
       grid_wait(&p.gc->arrive[2], G, abort, p.ew, 407);
     }
-    stage_wait(&sm->weighted, 0, abort, p.ew, 411);
+    const bool listed = stage_wait(&sm->weighted, 0, abort, p.ew, 411);
     consumer_sync();
 
     // ---------------- combine, slot order then the shared expert ----------------
     const int d4 = p.d / 4;
-    for (int i = blockIdx.x * kConsumers + tid; i < p.T * d4; i += G * kConsumers) {
+    for (int i = listed && !*abort ? blockIdx.x * kConsumers + tid : p.T * d4; i < p.T * d4; i += G * kConsumers) {
       const int t = i / d4, f = (i - t * d4) * 4;
       float4 v[kMaxRouteTopk];
 #pragma unroll
@@ -1141,6 +1179,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // the last CTA to get here leaves the grid's counters at zero (nobody waits on them any more)
   __syncwarp();
   __syncthreads();
+  if (*abort && warp >= kConsumerWarps && warp < kConsumerWarps + kGroups)
+    drain(sm, p.stages, warp - kConsumerWarps, lane);
   if (tid == 0) sm->last = atomicAdd(&p.gc->done, 1) == G - 1;
   __syncthreads();
   if (sm->last) {

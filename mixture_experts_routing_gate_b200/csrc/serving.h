@@ -16,6 +16,14 @@ struct GridCounters {
 constexpr size_t kErrorBytes = 256, kControlBytes = 4096;   // ErrorWord; both together
 static_assert(kErrorBytes + sizeof(GridCounters) <= kControlBytes, "the workspace's first region");
 
+// What the failure-detection test hook makes a serving kernel do.
+enum Stall {
+  kStallCopies = 1,   // the producers issue no copies
+  kStallRouter = 2,   // the router warps build no lists
+  kStallLater = 3,    // the producers issue five stages of copies each, and no more
+  kStallOneCta = 4    // those of the first CTA alone
+};
+
 // The whole layer for a few tokens (decode.cu).
 constexpr int kDecodeMaxTokens = MOE_DECODE_MAX_TOKENS;
 struct DecodeParams {
@@ -26,7 +34,7 @@ struct DecodeParams {
   int vocab;                  // > 0 with token_ids and tid2eid: the token-id table routes
   int gate_splits;            // slices of k of the router logits
   int stages;                 // of a weight ring (set by the launcher)
-  int test_stall;             // failure-detection test hook: the producers issue no loads
+  int test_stall;             // failure-detection test hook, one of Stall (0 outside the test build)
   const int32_t* token_ids;   // [T] or null
   const int32_t* tid2eid;     // [vocab, k]
   const float* w_gate;        // [E, d]

@@ -398,3 +398,37 @@ def test_decode_stall_times_out_and_the_workspace_recovers(M, monkeypatch, mxfp4
             hooks.moe_test_set_stall(0)
         assert st == M.MOE_ERR_TIMEOUT and 400 <= info <= 410, (st, info)
         _check_gated(M, cfg, li, w4, ws)
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
+@pytest.mark.parametrize("T", [2, 16])
+@pytest.mark.parametrize("stall", [2, 3, 4])
+def test_decode_waits_given_up_midway(M, monkeypatch, stall, T, mxfp4):
+    # the test build: the lists never come (2), or the copies end in the middle of a tile, in every CTA (3) or in
+    # the first alone (4).  The call ends with a timeout and writes its outputs at most; the next ones are right
+    hooks = M.load_library(B.build(test_hooks=True))
+    hooks.moe_test_set_stall.argtypes = [ctypes.c_int]
+    hooks.moe_test_set_stall.restype = None
+    cfg = TINY.replace(T=T, dim=8192, inter_dim=1024)
+    li, w4 = _layer(cfg, mxfp4)
+    with monkeypatch.context() as m:
+        m.setattr(M, "lib", hooks)
+        desc = M.layer_desc(cfg)
+        ws = M.Workspace(desc, T)
+        behind = ws.buf[ws.tensor.data_ptr() - ws.buf.data_ptr() + ws.nbytes:]
+        behind.fill_(165)
+        buf = torch.full((T + 2, cfg.dim), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = buf[1:T + 1]
+        weights = (w4,) if mxfp4 else (li.w1, li.w3, li.w2)
+        call = M.moe_decode_mxfp4 if mxfp4 else M.moe_decode
+        hooks.moe_test_set_stall(stall)
+        try:
+            call(desc, li.x, li.w_gate, *weights, y, ws, bias=li.bias)
+            st, info = M.moe_get_error(ws)
+        finally:
+            hooks.moe_test_set_stall(0)
+        assert st == M.MOE_ERR_TIMEOUT and 400 <= info <= 411, (st, info)
+        assert bool((buf[0] == 7.0).all()) and bool((buf[T + 1] == 7.0).all()) and bool((behind == 165).all())
+        assert int(ws.tensor[:4096].count_nonzero()) == 0    # the control words of the next call
+        for _ in range(2):
+            _check_gated(M, cfg, li, w4, ws)
