@@ -134,6 +134,7 @@ template <int kNT>
 struct StreamSmem {
   uint64_t full[kStreamMaxStages], empty[kStreamMaxStages];
   int abort, last;
+  int issued;   // stages whose copies the producer has started
   alignas(16) float red[8][8 * kNT][kStreamPitch];
 };
 
@@ -179,17 +180,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   if (tid == 0) {
     sm->abort = 0;
+    sm->issued = 0;
     tma_prefetch_desc(&map_w);
   }
   __syncthreads();
   pdl_begin();
 
   if (warp == kStreamWarps) {
-    if (lane == 0 && !p.test_stall) {
+    if (lane == 0 && p.test_stall != kStallCopies) {
+      const int most = p.test_stall == kStallLater ? 5 : 0x7fffffff;
       int slot = 0, issued = 0;
       uint32_t ph = 0;
       int row = u0 / ns * kStreamRows, k = u0 % ns * kStreamK;
-      for (int u = u0; u < u1; ++u) {
+      for (int u = u0; u < u1 && issued < most; ++u) {
         if (!mbar_wait(&sm->empty[slot], ph ^ 1, abort, p.ew, 501)) break;
         uint8_t* dst = ring + slot * kStreamBytes;
         mbar_arrive_expect_tx(&sm->full[slot], kStreamBytes);   // whole boxes: zeros past K and N
@@ -205,9 +208,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           ph ^= 1;
         }
       }
-      if (*abort)   // let every copy already issued land before the CTA leaves
-        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-          mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+      sm->issued = issued;
     }
   } else {
     const int grp = warp >> 3, wk = warp & 3, wr = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int slot = grp % p.stages;
     uint32_t ph = 0;
     if (u0 + grp < u1) fetch(u0 + grp);
+    bool lost = false;   // a wait of this warp was given up: it frees no stage any more, whose fill may be under way
     for (int u = u0; u < u1;) {
       const int tile = u / ns, end = min((tile + 1) * ns, u1);
       const bool starts = u == tile * ns, ends = end == (tile + 1) * ns;
@@ -233,8 +235,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) cur[nt] = nxt[nt];
         if (s + 2 < u1) fetch(s + 2);
-        if (!mbar_try_wait(&sm->full[slot], ph) && !*abort) mbar_wait(&sm->full[slot], ph, abort, p.ew, 502);
-        __syncwarp();
+        const bool got = !lost && (mbar_try_wait(&sm->full[slot], ph) ||
+                                   (!*abort && mbar_wait(&sm->full[slot], ph, abort, p.ew, 502)));
+        lost = !__all_sync(0xffffffffu, got);
+        if (lost) break;
         // elements [32 wk, 32 wk + 32) are half of 64-element column wk / 2
         const uint32_t at = ring_addr + slot * kStreamBytes + (wk >> 1) * (kStreamBytes / 2) +
                             (wr * 32 + g) * 128 + ((((wk & 1) * 4 + t) ^ g) << 4);
@@ -323,6 +327,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   __syncwarp();
   __syncthreads();
+  if (*abort && tid == kStreamConsumers) {   // every copy already started lands before the CTA leaves
+    for (int i = sm->issued > p.stages ? sm->issued - p.stages : 0; i < sm->issued; ++i)
+      mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -357,6 +365,7 @@ struct LinGemmSmem {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  int issued;   // stages that the producer has filled
   alignas(16) float stage[kEpiWarps][32 * kEpiPitch];
 };
 
@@ -419,6 +428,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     mbar_init(&sm->drain, 1);
     sm->abort = 0;
+    sm->issued = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_w);
@@ -443,19 +453,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (lane == 0) {
       int st = 0;
       uint32_t ph = 0;
-      int last_par[kGemmStagesMax];
-      for (int s = 0; s < kGemmStagesMax; ++s) last_par[s] = -1;
+      int issued = 0;
+      const int most = p.test_stall == kStallLater ? 3 : 0x7fffffff;
       const uint32_t full_leader = kPair ? cluster_addr(&sm->full[0], 0) : 0u;   // + 8 * stage
-      bool ok = p.test_stall == 0;
+      bool ok = p.test_stall != kStallCopies;
       for (int w = first; w < units && ok; w += step) {
         const LinUnit u = lin_unit(p, w);
         const int row_x = (u.m * L::kCtas + (int)rank) * 128, row_w = u.n * L::kBN + (int)rank * (L::kBN / L::kCtas);
         for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!mbar_wait(&sm->empty[st], ph ^ 1, abort, p.ew, 511)) {
+          if (issued == most || !mbar_wait(&sm->empty[st], ph ^ 1, abort, p.ew, 511)) {
             ok = false;
             break;
           }
-          last_par[st] = (int)ph;
+          ++issued;
           uint8_t* sa = smem + st * stage_bytes;
           if (leader) mbar_arrive_expect_tx(&sm->full[st], L::kCtas * stage_bytes);   // whole boxes: zeros outside
           if (kPair) {
@@ -471,9 +481,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
-      if (*abort && leader)   // let every load already issued land before the CTA can exit
-        for (int s = 0; s < p.stages; ++s)
-          if (last_par[s] >= 0) mbar_wait(&sm->full[s], last_par[s], nullptr, nullptr, 0, 200000000LL);
+      sm->issued = issued;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -683,7 +691,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
+  // A wait was given up: every load already started lands before a CTA leaves (a pair's, on the even CTA's barriers).
+  if (*abort && leader && threadIdx.x == 0)
+    for (int i = sm->issued > p.stages ? sm->issued - p.stages : 0; i < sm->issued; ++i)
+      mbar_wait(&sm->full[i % p.stages], (i / p.stages) & 1, nullptr, nullptr, 0, 200000000LL);
+  __syncwarp();
   if (kPair) cluster_sync();  // no remote signal or MMA of either CTA is outstanding past this point
   if (*abort) {
     // a wait ran out: give any TMA copy this CTA may still have in flight time to land

@@ -20,7 +20,7 @@ static_assert(kErrorBytes + sizeof(GridCounters) <= kControlBytes, "the workspac
 enum Stall {
   kStallCopies = 1,   // the producers issue no copies
   kStallRouter = 2,   // the router warps build no lists
-  kStallLater = 3,    // the producers issue five stages of copies each, and no more
+  kStallLater = 3,    // the producers issue a few stages of copies each (inside a tile), and no more
   kStallOneCta = 4    // those of the first CTA alone
 };
 
@@ -74,7 +74,7 @@ struct LinearParams {
   int stages;                 // set by the launcher
   int m_tiles, n_tiles, splits;
   int x_box;                  // rows of x per tile in shared memory
-  int test_stall;
+  int test_stall;             // as DecodeParams::test_stall (kStallCopies, kStallLater)
   long long ldx, ldy, ldr;    // elements
   const __nv_bfloat16* x;
   const float* bias;          // [N] or null

@@ -264,3 +264,34 @@ def test_decode_step_of_a_block(M):
     assert float((y.float() - y2.float()).abs().max()) <= 4e-2 * rms
     M.check_device_errors(wd)
     M.check_device_errors(wl)
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 7168, 7168), (16, 7168, 7168), (20, 7168, 64), (100, 7168, 300), (700, 2048, 5000),
+                                   (4096, 1024, 4096)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_waits_given_up_midway(M, monkeypatch, T, K, N, out):
+    # the test build's producers stop inside a tile: the call ends with a timeout, writes y at most, and the
+    # same workspace serves the next one
+    hooks = M.load_library(B.build(test_hooks=True))
+    hooks.moe_test_set_stall.argtypes = [ctypes.c_int]
+    hooks.moe_test_set_stall.restype = None
+    x, w = _normal((T, K), 1.0, 3), _normal((N, K), 1.0 / math.sqrt(K), 4)
+    buf = torch.full((T + 2, N + 8), 7.0, dtype=out, device="cuda")
+    y = buf[1:T + 1, :N]
+    with monkeypatch.context() as m:
+        m.setattr(M, "lib", hooks)
+        desc = M.linear_desc(K, N, out_dtype=out)
+        ws = M.LinearWorkspace(desc, T)
+        hooks.moe_test_set_stall(3)
+        try:
+            M.moe_linear(desc, x, w, y, ws)
+            st, info = M.moe_get_error(ws)
+        finally:
+            hooks.moe_test_set_stall(0)
+        assert st == M.MOE_ERR_TIMEOUT and 500 <= info <= 520, (st, info)
+        assert int(ws.tensor[:4096].count_nonzero()) == 0
+        for _ in range(2):
+            M.moe_linear(desc, x, w, y, ws)
+            M.check_device_errors(ws)
+            _check(y, x, w, "none", None, None)
+        assert bool((buf[0] == 7.0).all()) and bool((buf[T + 1] == 7.0).all()) and bool((buf[:, N:] == 7.0).all())
