@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -96,10 +97,12 @@ struct DecodeSmem {
   uint64_t full[kGroups][kMaxStages];
   uint64_t empty[kGroups][kMaxStages];
   uint64_t routed, weighted;        // the lists below are complete; the slots' weights are too
-  int abort, last;
+  int abort;
+  int n_act;                        // the lists' experts as published with `routed` (0 before); follows `abort`
+  int last;
   int up_done[kGroups];             // warps that wrote their part of an up tile's h, over the group's tiles so far
   int issued[kGroups];              // stages whose copies a group's producer has started
-  int n_act;                        // active experts, the shared one first
+  int n_listed;                     // active experts, the shared one first
   int sel_e[kMaxS];
   float sel_w[kMaxS];
   int dup[kMaxS];                   // the token already chose this expert in an earlier slot
@@ -131,20 +134,6 @@ __device__ __forceinline__ void router_sync() {
 __device__ __forceinline__ void group_sync(int group) {
   __syncwarp();
   asm volatile("bar.sync %0, 256;" ::"r"(3 + group) : "memory");
-}
-// group_sync that tells every warp of the group whether one of them says so.
-__device__ __forceinline__ bool group_any(int group, bool v) {
-  int any;
-  __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.s32 p, %2, 0;\n\t"
-      "bar.red.or.pred q, %1, 256, p;\n\t"
-      "selp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(3 + group), "r"((int)v)
-      : "memory");
-  return any != 0;
 }
 static_assert(kConsumers == 512 && kRouters == 64 && kGroupThreads == 256, "the named barriers' thread counts");
 
@@ -181,14 +170,21 @@ __device__ __forceinline__ bool grid_wait(const int* counter, int target, volati
   }
 }
 
-// A consumer warp's wait: the usual, successful test inline; after an abort no waiting at all.  False, in every
-// lane alike, where a lane's wait was given up.
-__device__ __noinline__ bool stage_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
-  return !*abort && mbar_wait(bar, parity, abort, ew, site);
+// A consumer's wait: the usual, successful test inline; after an abort no waiting at all.  A warp that gives up
+// the wait for the lists publishes empty ones (the shared expert alone) in n_act, the word behind `abort`, unless
+// the router has just published its own: all warps go by the same lists.  (It is here, and not where the lists
+// are waited for, since what is added between two tiles costs the four-bit layer 3 to 5 us of 75.)
+constexpr int kListsSite = 409;
+__device__ __noinline__ void stage_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  const bool got = !*abort && mbar_wait(bar, parity, abort, ew, site);
+  if (!got && site == kListsSite) {
+    if (atomicCAS(const_cast<int*>(abort) + 1, 0, 1) == 0) mbar_arrive(bar);
+    __threadfence_block();
+  }
 }
-__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
-  const bool got = mbar_try_wait(bar, parity) || stage_wait_slow(bar, parity, abort, ew, site);
-  return __all_sync(0xffffffffu, got);
+__device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, ErrorWord* ew, int site) {
+  if (!mbar_try_wait(bar, parity)) stage_wait_slow(bar, parity, abort, ew, site);
+  __syncwarp();
 }
 
 template <bool kF16>
@@ -565,7 +561,7 @@ __device__ __forceinline__ void build_lists(const DecodeParams& p, Smem* sm, int
       const int v = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += v;
     }
-    if (lane == 31) sm->n_act = 1 + (run >> 16);
+    if (lane == 31) sm->n_listed = 1 + (run >> 16);
     run -= mine;
     for (int e = e0; e < e1; ++e) {
       const uint32_t m = sm->mask[e];
@@ -595,6 +591,13 @@ __device__ __forceinline__ void build_lists(const DecodeParams& p, Smem* sm, int
   router_sync();
   for (int s = rt; s < S; s += kRouters) sm->mask[sm->sel_e[s]] = 0u;
   router_sync();
+}
+
+// The lists are there for all (unless a consumer that gave up has published empty ones).
+template <typename Smem>
+__device__ __forceinline__ void publish_lists(Smem* sm) {
+  __threadfence_block();
+  if (atomicCAS(&sm->n_act, 0, sm->n_listed) == 0) mbar_arrive(&sm->routed);
 }
 
 // The router warps: selection and lists, then the CTA's reports of finished up tiles.
@@ -629,7 +632,7 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
     }
     router_sync();
     build_lists(p, sm, rt, lane);
-    if (rt == 0) mbar_arrive(&sm->routed);
+    if (rt == 0) publish_lists(sm);
   }
   if (lane == 0) grid_wait(&p.gc->arrive[0], (int)gridDim.x, abort, p.ew, 404);
   __syncwarp();
@@ -658,7 +661,7 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
   router_sync();
   if (!early) {
     build_lists(p, sm, rt, lane);
-    if (rt == 0) mbar_arrive(&sm->routed);
+    if (rt == 0) publish_lists(sm);
   }
   if (rt == 0) mbar_arrive(&sm->weighted);
   if (blockIdx.x == 0) {
@@ -678,12 +681,12 @@ __device__ __forceinline__ void route(const DecodeParams& p, Smem* sm, int rw, i
   if (lane == 0) {   // a router warp for each group
     const int nb = p.I / Stage<kFp4>::kUp;
     const long long t0 = clock64();
-    int seen = 0;
-    for (TileIter it(nb, (int)blockIdx.x * kGroups + rw, (int)gridDim.x * kGroups); it.a < sm->n_act;) {
+    int seen = 0;   // n_listed: n_act is published by one of these lanes, for the others
+    for (TileIter it(nb, (int)blockIdx.x * kGroups + rw, (int)gridDim.x * kGroups); it.a < sm->n_listed;) {
       // a tile's writers are all past the tile before it, so the count passes each tile's total in turn
       const int done = *(volatile int*)&sm->up_done[rw];
       int tiles = 0;
-      for (; it.a < sm->n_act && done >= seen + up_writers<kFp4>(sm->act_n[it.a]); it.next()) {
+      for (; it.a < sm->n_listed && done >= seen + up_writers<kFp4>(sm->act_n[it.a]); it.next()) {
         if (tiles++ == 0) __threadfence();
         seen += up_writers<kFp4>(sm->act_n[it.a]);
         atomicAdd(&p.gc->ready[it.a], 1);
@@ -856,24 +859,27 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const CUtensorMap
   RingPos pos;
   int issued = 0;
   bool ok = true, routed = false;
+  // A free stage to fill: none once a wait has been given up.
+  auto free_stage = [&]() {
+    int ok = 0;
+    if (!kFp4 || lane == 0) ok = mbar_wait(&empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401) && !*abort;
+    return (kFp4 ? __shfl_sync(0xffffffffu, ok, 0) : ok) != 0;
+  };
   auto tile = [&](bool down, int e, int blk) {
     const int K = down ? p.I : p.d;
     const int row = down ? e * p.d + blk * S::kRows : e * p.I + blk * S::kUp;
     const CUtensorMap *m0 = down ? map_w2 : map_w1, *m1 = down ? map_w2 : map_w3;
     const int row1 = down ? row + S::kRows / 2 : row;
     for (int k0 = 0; k0 < K; k0 += S::kChunk) {
-      if (issued == most) return false;
+      if (issued == most || !free_stage()) return false;
       uint64_t* bar = &full[pos.slot];
       uint8_t* dst = ring + pos.slot * S::kBytes;
       if (kFp4) {
-        if (!mbar_wait_warp(&empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) return false;
         const uint8_t* s0 = down ? p.w2s : p.w1s;
         const uint8_t* s1 = down ? p.w2s : p.w3s;
         cp_async16(smem_u32(dst + S::kSOff + lane * 16), s0 + ((size_t)(row + lane) * K + k0) / 32);
         cp_async16(smem_u32(dst + S::kSOff + (32 + lane) * 16), s1 + ((size_t)(row1 + lane) * K + k0) / 32);
         cp_async_arrive(bar);
-      } else if (!mbar_wait(&empty[pos.slot], pos.phase ^ 1, abort, p.ew, 401)) {
-        return false;
       }
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, 2 * S::kBlock);   // whole boxes: what lies past K is filled with zeros
@@ -927,6 +933,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Smem* sm = reinterpret_cast<Smem*>(ring + kGroups * p.stages * S::kBytes);
+  static_assert(offsetof(Smem, n_act) == offsetof(Smem, abort) + sizeof(int), "where stage_wait_slow finds it");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   if (tid < kGroups * p.stages) {
     mbar_init(&sm->full[tid / p.stages][tid % p.stages], kFp4 ? 1 + 32 : 1);
@@ -937,7 +944,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     mbar_init(&sm->routed, 1);
     mbar_init(&sm->weighted, 1);
     sm->abort = 0;
-    sm->n_act = 1;
+    sm->n_act = 0;
     for (int i = 0; i < kGroups; ++i) sm->up_done[i] = sm->issued[i] = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_w1);
@@ -959,10 +966,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   __syncthreads();
 
-  // Every wait below is bounded.  A consumer warp whose wait was given up touches nothing any more: it neither
-  // reads the lists (which may not exist) nor frees a stage (whose fill may be under way: a second fill would
-  // arm its barrier twice).  It goes on to the next barrier of its group and says so there, and the whole group
-  // leaves the tiles at that barrier.  The combine is left out, and the producers see their copies land.
+  // Every wait below is bounded.  After one was given up the consumers go on over whatever lies in the ring, so
+  // that they keep meeting at the same barriers; what they free then may still be under way, so the producers fill
+  // nothing any more once `abort` is set (a consumer that gave up has seen it set before it frees the stage).
+  // The lists that they go by are published once, by the router or (empty) by the first that gave up waiting for
+  // them.  The combine is left out after an abort, and the producers see their copies land.
   volatile int* abort = &sm->abort;
   const int G = (int)gridDim.x;
   if (warp >= kConsumerWarps && warp < kConsumerWarps + kGroups) {
@@ -1001,24 +1009,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       int ready_a = -1;
       bool all_ready = !kDown;
       // Whether the iterator stands on a tile (waits for the lists at the first routed one).
-      bool lost = false;   // a wait of this warp was given up
       auto live = [&]() {
         if (it.a > 0 && !routed) {
-          routed = stage_wait(&sm->routed, 0, abort, p.ew, 409);
-          lost |= !routed;
+          stage_wait(&sm->routed, 0, abort, p.ew, kListsSite);
+          routed = true;
         }
-        return it.a == 0 || (routed && it.a < sm->n_act);
+        return it.a == 0 || it.a < sm->n_act;
       };
       auto enter = [&]() {
         if (!all_ready && it.a != ready_a) {   // all of this expert's h is written?
-          int done = 0;   // 1: of this expert, 2: of all
+          int done = 0;
           if (lane == 0) {
-            if (ld_acquire(&p.gc->arrive[1]) >= sm->n_act * nb1) done = 2;
-            else done = grid_wait(&p.gc->ready[it.a], nb1, abort, p.ew, 402);
+            done = ld_acquire(&p.gc->arrive[1]) >= sm->n_act * nb1;
+            if (!done) grid_wait(&p.gc->ready[it.a], nb1, abort, p.ew, 402);
           }
-          done = __shfl_sync(0xffffffffu, done, 0);
-          all_ready = done == 2;
-          lost |= done == 0;
+          all_ready = __shfl_sync(0xffffffffu, done, 0) != 0;
           ready_a = it.a;
         }
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a];
@@ -1069,13 +1074,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
       }
-      if (group_any(grp, lost)) return false;
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
         auto one_stage = [&](int s, TokenFrags<kFp4, kNT, kLo>& tok) {
-          lost = lost || !stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
-          if (lost) return;
+          stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
             const uint32_t stage = ring_addr + pos.slot * S::kBytes;
             if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
@@ -1091,7 +1094,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         // the next tile's first fragments are under way while this one is added up
         it.next();
-        more = !lost && live();
+        more = live();
         if (more) {
           enter();
 #pragma unroll
@@ -1100,7 +1103,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         float* red = sm->red[grp][buf];
         if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
         put_partials<kFp4, kNT>(red, w8, lane, acc, n <= 8 ? 1 : 2);
-        if (group_any(grp, lost)) return false;
+        group_sync(grp);
         if constexpr (kDown) {
           for (int i = gtid; i < n * S::kRows; i += kGroupThreads) {
             const int c = i / S::kRows, r = i % S::kRows;
@@ -1139,21 +1142,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         if (!kTwo) group_sync(grp);
       }
-      return true;
     };
-    if (run_phase(std::false_type{}, TileIter(nb1, self, all)))
-      run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
+    run_phase(std::false_type{}, TileIter(nb1, self, all));
+    run_phase(std::true_type{}, down_tiles(p, sm->n_act, nb1, nb2, self, all));
     consumer_sync();
     if (tid == 0) {   // after an abort too: the other CTAs are not kept waiting
       red_release_add(&p.gc->arrive[2], 1);
       grid_wait(&p.gc->arrive[2], G, abort, p.ew, 407);
     }
-    const bool listed = stage_wait(&sm->weighted, 0, abort, p.ew, 411);
+    const bool weighted = mbar_wait(&sm->weighted, 0, abort, p.ew, 411);
     consumer_sync();
 
     // ---------------- combine, slot order then the shared expert ----------------
     const int d4 = p.d / 4;
-    for (int i = listed && !*abort ? blockIdx.x * kConsumers + tid : p.T * d4; i < p.T * d4; i += G * kConsumers) {
+    for (int i = weighted && !*abort ? blockIdx.x * kConsumers + tid : p.T * d4; i < p.T * d4; i += G * kConsumers) {
       const int t = i / d4, f = (i - t * d4) * 4;
       float4 v[kMaxRouteTopk];
 #pragma unroll

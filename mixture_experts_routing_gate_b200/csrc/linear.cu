@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       uint32_t ph = 0;
       int row = u0 / ns * kStreamRows, k = u0 % ns * kStreamK;
       for (int u = u0; u < u1 && issued < most; ++u) {
-        if (!mbar_wait(&sm->empty[slot], ph ^ 1, abort, p.ew, 501)) break;
+        // A consumer whose wait was given up goes on and frees stages whose fill may be under way, but has seen
+        // `abort` set before: a second fill would arm the barrier twice.
+        if (!mbar_wait(&sm->empty[slot], ph ^ 1, abort, p.ew, 501) || *abort) break;
         uint8_t* dst = ring + slot * kStreamBytes;
         mbar_arrive_expect_tx(&sm->full[slot], kStreamBytes);   // whole boxes: zeros past K and N
         tma_load_2d(dst, &map_w, &sm->full[slot], k, row);
@@ -225,7 +227,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int slot = grp % p.stages;
     uint32_t ph = 0;
     if (u0 + grp < u1) fetch(u0 + grp);
-    bool lost = false;   // a wait of this warp was given up: it frees no stage any more, whose fill may be under way
     for (int u = u0; u < u1;) {
       const int tile = u / ns, end = min((tile + 1) * ns, u1);
       const bool starts = u == tile * ns, ends = end == (tile + 1) * ns;
@@ -235,10 +236,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) cur[nt] = nxt[nt];
         if (s + 2 < u1) fetch(s + 2);
-        const bool got = !lost && (mbar_try_wait(&sm->full[slot], ph) ||
-                                   (!*abort && mbar_wait(&sm->full[slot], ph, abort, p.ew, 502)));
-        lost = !__all_sync(0xffffffffu, got);
-        if (lost) break;
+        if (!mbar_try_wait(&sm->full[slot], ph) && !*abort) mbar_wait(&sm->full[slot], ph, abort, p.ew, 502);
+        __syncwarp();
         // elements [32 wk, 32 wk + 32) are half of 64-element column wk / 2
         const uint32_t at = ring_addr + slot * kStreamBytes + (wk >> 1) * (kStreamBytes / 2) +
                             (wr * 32 + g) * 128 + ((((wk & 1) * 4 + t) ^ g) << 4);
