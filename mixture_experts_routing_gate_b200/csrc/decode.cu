@@ -145,6 +145,11 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 __device__ __forceinline__ void red_release_add(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+__device__ __forceinline__ int atom_acquire_add(int* p, int v) {
+  int old;
+  asm volatile("atom.acquire.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
 // 16 bytes global -> shared past L1, and this lane's arrival on a barrier once its copies so far landed.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -978,6 +983,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (kFp4 || lane == 0) produce<kFp4>(p, &map_w1, &map_w3, &map_w2, sm, ring + grp * p.stages * S::kBytes, grp, lane);
   } else if (warp >= kConsumerWarps + kGroups) {
     route<kFp4>(p, sm, warp - kConsumerWarps - kGroups, lane);
+    if (lane == 0) red_release_add(&p.gc->done, 1);
   } else {
     gate_partials<kNT>(p, sm->red[0][0], warp, lane);
     if (kFp4) scale_tokens(p, tid);
@@ -1178,12 +1184,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           make_uint2(bf16x2_bits(y.x + sh.x, y.y + sh.y), bf16x2_bits(y.z + sh.z, y.w + sh.w));
     }
   }
-  // the last CTA to get here leaves the grid's counters at zero (nobody waits on them any more)
+  // The last CTA to get here leaves the grid's counters at zero.  Nobody waits on them any more, but a tile's
+  // report that nobody waited for (it is passed over once the total is there) must not land behind the zeros.
+  // So the lanes that report have arrived on `done` themselves, by a release behind their reports, which the last
+  // CTA's arrival acquires; the other counters' sums it has waited for.
   __syncwarp();
   __syncthreads();
   if (*abort && warp >= kConsumerWarps && warp < kConsumerWarps + kGroups)
     drain(sm, p.stages, warp - kConsumerWarps, lane);
-  if (tid == 0) sm->last = atomicAdd(&p.gc->done, 1) == G - 1;
+  if (tid == 0) {
+    if (*abort) __threadfence();   // it may not have waited
+    sm->last = atom_acquire_add(&p.gc->done, 1) == (1 + kRouterWarps) * G - 1;
+  }
   __syncthreads();
   if (sm->last) {
     if (tid < kMaxAct) p.gc->ready[tid] = 0;

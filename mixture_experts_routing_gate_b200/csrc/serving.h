@@ -9,7 +9,7 @@ namespace moe {
 // The control words behind the error word at the head of a workspace, all zero between calls.
 struct GridCounters {
   int arrive[4];        // the one-launch layer's grid counters: logits, up tiles, down, tokens
-  int done;             //   CTAs finished
+  int done;             //   CTAs and their reporting lanes finished
   int ready[144];       //   up tiles finished, per active expert
   int linear_done[512]; // the linear projection's parts of a tile finished
 };

@@ -432,3 +432,19 @@ def test_decode_waits_given_up_midway(M, monkeypatch, stall, T, mxfp4):
         assert int(ws.tensor[:4096].count_nonzero()) == 0    # the control words of the next call
         for _ in range(2):
             _check_gated(M, cfg, li, w4, ws)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_decode_leaves_the_control_words_at_zero(M, T):
+    # calls one after another on one workspace find the grid's counters at zero, and so does what follows
+    cfg = TINY.replace(T=T, n_experts=64, inter_dim=512)
+    li, _ = _layer(cfg)
+    desc = M.layer_desc(cfg)
+    ws = M.Workspace(desc, T)
+    y = torch.empty_like(li.x)
+    left = torch.zeros(400, dtype=torch.int64, device="cuda")
+    for i in range(400):
+        M.moe_decode(desc, li.x, li.w_gate, li.w1, li.w3, li.w2, y, ws, bias=li.bias)
+        left[i] = ws.tensor[:4096].count_nonzero()
+    assert int(left.sum()) == 0
+    _check_gated(M, cfg, li, None, ws)
