@@ -105,7 +105,8 @@ typedef struct {
                                      the default E4M3 activations on the block-scaled tensor cores.
                                      Unlike the other options this one changes the values computed. */
 
-/* Bytes of workspace needed by any entry point below for a batch of T tokens. */
+/* Bytes of workspace needed by any entry point below for a batch of T tokens.  They never fall as T grows: a
+ * workspace for T tokens serves every smaller batch of the same layer too. */
 size_t moe_workspace_bytes(const moe_layer_desc* desc, int T);
 
 /* Clears the workspace's control words (the error word, dispatch's block counter and the serving calls'

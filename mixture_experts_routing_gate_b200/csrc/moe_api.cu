@@ -84,6 +84,7 @@ namespace {
 struct WsLayout {
   size_t err, flag, planes, indices, weights, counts, offsets, row_of_slot, tok_of_row, w_perm, hist, base,
       chunk_prefix, x_perm, h, out_perm, out_shared, xq, dec_partial, dec_out, dec_x16, dec_x_scale, dec_h_scale, dec_h, total;
+  size_t staged;                           // bytes that the entry points other than the one-launch layer need
   size_t xp_scales, h_scales, xq_scales;   // offsets of the scales inside x_perm, h and xq
 };
 
@@ -121,14 +122,16 @@ WsLayout ws_layout(const moe_layer_desc& d, int T) {
   L.out_shared = take((size_t)T * D * 2);
   L.xq = take(codes_and_scales((size_t)T * D));
   L.xq_scales = L.xq + align_up((size_t)T * D);
-  // the one-launch layer's partial logits and fp32 expert rows (batches it takes only)
-  const bool dec = T <= MOE_DECODE_MAX_TOKENS;
-  L.dec_partial = take(dec ? (size_t)moe::decode_gate_splits(d.n_experts, d.dim) * T * E * 4 : 0);
-  L.dec_out = take(dec ? (S + T) * D * 4 : 0);
-  L.dec_x16 = take(dec ? (size_t)T * D * 2 : 0);
-  L.dec_x_scale = take(dec ? (size_t)T * (D / 32) * 4 : 0);
-  L.dec_h = take(dec ? 2 * (S + T) * I * 2 : 0);
-  L.dec_h_scale = take(dec ? (S + T) * (I / 32) * 4 : 0);
+  L.staged = o;
+  // The one-launch layer's partial logits and fp32 expert rows.  Larger batches hold room for the largest that it
+  // takes, so that a workspace serves every smaller batch too: no region shrinks as T grows.
+  const size_t t = std::min(T, MOE_DECODE_MAX_TOKENS), rows = t * d.topk + t;
+  L.dec_partial = take((size_t)moe::decode_gate_splits(d.n_experts, d.dim) * t * E * 4);
+  L.dec_out = take(rows * D * 4);
+  L.dec_x16 = take(t * D * 2);
+  L.dec_x_scale = take(t * (D / 32) * 4);
+  L.dec_h = take(2 * rows * I * 2);
+  L.dec_h_scale = take(rows * (I / 32) * 4);
   L.total = o;
   return L;
 }
@@ -138,9 +141,10 @@ Ptr* at(void* ws, size_t off) {
   return reinterpret_cast<Ptr*>(static_cast<uint8_t*>(ws) + off);
 }
 
-moe_status check_ws(const moe_layer_desc& d, int T, void* ws, size_t ws_bytes) {
+moe_status check_ws(const moe_layer_desc& d, int T, void* ws, size_t ws_bytes, bool one_launch = false) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_WORKSPACE;
-  if (ws_bytes < ws_layout(d, T).total) return MOE_ERR_WORKSPACE;
+  const WsLayout L = ws_layout(d, T);
+  if (ws_bytes < (one_launch ? L.total : L.staged)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -876,7 +880,7 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   if (T > 0 && fp4 == nullptr && (w1 == nullptr || w3 == nullptr || w2 == nullptr)) return MOE_ERR_INVALID;
   if (T > 0 && (!aligned16(x) || !aligned16(w_gate) || !aligned16(y))) return MOE_ERR_INVALID;
   if (T > 0 && fp4 == nullptr && (!aligned16(w1) || !aligned16(w3) || !aligned16(w2))) return MOE_ERR_INVALID;
-  MOE_TRY(check_ws(*desc, T, ws, ws_bytes));
+  MOE_TRY(check_ws(*desc, T, ws, ws_bytes, true));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) {
     if (counts_out != nullptr) return cuda_status(cudaMemsetAsync(counts_out, 0, sizeof(int32_t) * desc->n_experts, s));

@@ -448,3 +448,14 @@ def test_decode_leaves_the_control_words_at_zero(M, T):
         left[i] = ws.tensor[:4096].count_nonzero()
     assert int(left.sum()) == 0
     _check_gated(M, cfg, li, None, ws)
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
+def test_decode_on_the_workspace_of_a_larger_batch(M, mxfp4):
+    import dataclasses
+    cfg = TINY.replace(T=17, dim=512, inter_dim=512)
+    li, w4 = _layer(cfg, mxfp4)
+    ws = M.Workspace(M.layer_desc(cfg), 17)
+    for T in (16, 1):
+        part = dataclasses.replace(li, x=li.x[:T].contiguous())
+        _check_gated(M, cfg.replace(T=T), part, w4, ws)

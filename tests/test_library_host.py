@@ -424,3 +424,11 @@ def test_linear_rejects_bad_arguments_before_launch(moe):
         moe.linear_desc(64, 32, out_dtype=torch.float16)
     with pytest.raises(KeyError):
         moe.linear_desc(64, 32, activation="tanh")
+
+
+@pytest.mark.parametrize("name", ["tiny", "v3_decode", "v4_skew"])
+def test_workspace_for_a_batch_serves_every_smaller_one(moe, name):
+    cfg = W.CONFIGS[name]
+    d = moe.layer_desc(cfg)
+    sizes = [moe.moe_workspace_bytes(d, T) for T in [*range(700), 1024, 1025, 4096, 16384]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
