@@ -429,8 +429,8 @@ moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x
  * Needs K % 8 == 0 and ldx % 8 == 0 (MOE_ERR_UNSUPPORTED otherwise); x and w 16-byte aligned, the others
  * aligned to their elements, ldx >= K, ldy >= N, ldr >= N (MOE_ERR_INVALID otherwise).
  * ws: moe_linear_workspace_bytes(desc, T) bytes, 1 KiB aligned, cleared once by moe_workspace_init; a
- * workspace serves one call at a time, and any descriptor it is large enough for.  Results do not depend
- * on scheduling.
+ * workspace serves one call at a time, and any descriptor it is large enough for; one for T tokens serves
+ * fewer too.  Results do not depend on scheduling.
  */
 typedef enum {
   MOE_ACT_NONE = 0,

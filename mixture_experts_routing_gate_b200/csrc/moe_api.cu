@@ -935,10 +935,9 @@ moe_status check_linear(const moe_linear_desc* d, int T) {
   return MOE_OK;
 }
 
-// The linear projection's workspace: the control words, then the partials of cut tiles.
-size_t linear_ws_bytes(const moe_linear_desc& d, int T) {
-  const moe::LinearPlan plan = moe::linear_plan(T, d.in_features, d.out_features, num_sms());
-  return align_up(moe::kControlBytes) + align_up(plan.scratch_floats * sizeof(float));
+// The linear projection's workspace: the control words, then the partials of cut tiles, which small batches have.
+size_t linear_ws_bytes(size_t scratch_floats) {
+  return align_up(moe::kControlBytes) + align_up(scratch_floats * sizeof(float));
 }
 
 }  // namespace
@@ -1152,7 +1151,10 @@ moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x
 
 size_t moe_linear_workspace_bytes(const moe_linear_desc* desc, int T) {
   if (check_linear(desc, T) != MOE_OK) return 0;
-  return linear_ws_bytes(*desc, T);
+  // room for a batch that runs as a weight stream in every workspace: one for T tokens serves fewer too
+  const moe::LinearPlan most = moe::linear_plan(T, desc->in_features, desc->out_features, num_sms());
+  const moe::LinearPlan few = moe::linear_plan(0, desc->in_features, desc->out_features, num_sms());
+  return linear_ws_bytes(std::max(most.scratch_floats, few.scratch_floats));
 }
 
 moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int64_t ldx, const moe_bf16* w,
@@ -1173,7 +1175,7 @@ moe_status moe_linear(const moe_linear_desc* desc, int T, const moe_bf16* x, int
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_WORKSPACE;
   const int sms = num_sms();
   const moe::LinearPlan plan = moe::linear_plan(T, K, N, sms);
-  if (ws_bytes < align_up(moe::kControlBytes) + align_up(plan.scratch_floats * sizeof(float))) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < linear_ws_bytes(plan.scratch_floats)) return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;
   moe::LinearParams p{};
   p.T = T; p.K = K; p.N = N; p.act = d.activation; p.out_fp32 = d.out_fp32;

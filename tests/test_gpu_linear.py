@@ -295,3 +295,15 @@ def test_waits_given_up_midway(M, monkeypatch, T, K, N, out):
             M.check_device_errors(ws)
             _check(y, x, w, "none", None, None)
         assert bool((buf[0] == 7.0).all()) and bool((buf[T + 1] == 7.0).all()) and bool((buf[:, N:] == 7.0).all())
+
+
+def test_small_batches_on_the_workspace_of_a_large_one(M):
+    K, N = 1024, 1032
+    desc = M.linear_desc(K, N)
+    ws = M.LinearWorkspace(desc, 300)
+    w = _normal((N, K), 1.0 / math.sqrt(K), 4)
+    for T in (1, 16, 17, 300, 1):
+        x, y = _normal((T, K), 1.0, 3 + T), torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+        M.moe_linear(desc, x, w, y, ws)
+        M.check_device_errors(ws)
+        _check(y, x, w, "none", None, None)

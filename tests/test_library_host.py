@@ -432,3 +432,10 @@ def test_workspace_for_a_batch_serves_every_smaller_one(moe, name):
     d = moe.layer_desc(cfg)
     sizes = [moe.moe_workspace_bytes(d, T) for T in [*range(700), 1024, 1025, 4096, 16384]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("K,N", [(8, 1), (512, 512), (7168, 7168), (5120, 129280)])
+def test_linear_workspace_for_a_batch_serves_every_smaller_one(moe, K, N):
+    d = moe.linear_desc(K, N)
+    sizes = [moe.moe_linear_workspace_bytes(d, T) for T in [*range(400), 1024, 4096, 16384]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
