@@ -320,8 +320,9 @@ moe_status moe_forward(const moe_layer_desc* desc, int T, const moe_bf16* x, con
  * kernel launch for T <= MOE_DECODE_MAX_TOKENS (MOE_ERR_UNSUPPORTED above).  Made for decode batches,
  * where moe_forward's seven launches and their gaps cost more than the arithmetic: the whole grid is
  * resident and streams the chosen experts' weights without a break from the gate to the combine.
- * Values: the same formulas with fp32 accumulation; h is rounded once to bf16 (small layers: to 16 bits) and,
- * unlike in moe_forward, the expert outputs stay in fp32 until the combine.  Results do not depend on scheduling.
+ * Values: the same formulas with fp32 accumulation; unlike in moe_forward, h is held in two bf16 parts (off by at
+ * most 2^-16 of itself) and the expert outputs stay in fp32 until the combine.  Results do not depend on
+ * scheduling, nor a token's on the other tokens of its batch beyond the order of fp32 sums.
  * As in moe_forward, a hash-routed call uses neither bias nor logit_offset.
  * The selection may differ from moe_forward's where two experts' scores agree to fp32 rounding.
  * A table row that names an expert twice counts it twice (in the weights, in y and in counts_out).

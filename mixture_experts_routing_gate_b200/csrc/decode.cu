@@ -26,10 +26,11 @@
 //   expert's h is written (a counter per expert), with no barrier between the projections; CTAs that had one
 //   up tile less take more of the first down tiles.
 //
-// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is rounded to bf16, or held in two bf16
-// parts where that costs nothing (small layers; see the launcher).  Measured (floor at
-// the measured copy bandwidth in brackets): d = 7168, I = 2048, 9 experts, one token 132 us (122); d = 5120,
-// I = 1536, 16 tokens on 384 unevenly popular experts 327 to 377 us (278); d = 256, one token 18 us.
+// bf16 weights: tiles of 16 rows, 512 elements of k a stage, bf16 MMAs; h is held in two bf16 parts, in columns that
+// few tokens leave free (beside one rounded part: no time up to 8 tokens, 387 -> 403 us at 16; the error of y
+// against 64 bits 2.4e-3 -> 1.7e-3, its own rounding).  Measured (floor at the measured copy bandwidth in
+// brackets): d = 7168, I = 2048, 9 experts, one token 136 us (122); d = 5120, I = 1536, 16 tokens on 384 unevenly
+// popular experts 320 to 405 us, by the experts drawn (278); d = 256, one token 18 us.
 //
 // MXFP4 weights: what travels is a quarter, so the arithmetic of decoding is what has to be cheap.  The
 // hardware's E2M1 -> f16 conversion takes 73 codes/clock/SM (measured; the stream brings 44), where placing
@@ -712,10 +713,9 @@ static_assert(kRouterWarps == kGroups, "one reports for each group");
 // ------------------------------------------------------------------------------------------------
 // The warp's 64 elements of a stage's token rows (rows g and g + 8 of the tile's): two blocks of 32, of which
 // thread t holds 8 elements each; MXFP4: and the blocks' scales of the token columns 2t, 2t + 1 (+ 8).
-// bf16 h (kLo): and the second parts of its elements.
-template <bool kFp4, int kNT, bool kLo>
+template <bool kFp4, int kNT>
 struct TokenFrags {
-  uint4 v[kNT][2], lo[kLo ? kNT : 1][2];
+  uint4 v[kNT][2];
   float2 scale[kFp4 ? kNT : 1][2];   // .x, .y: the two blocks; of columns 2t and 2t + 1
 };
 
@@ -752,8 +752,8 @@ __device__ __noinline__ uint32_t clamp_scales(uint32_t s4, ErrorWord* ew) {
 }
 
 // w: the warp's place in its group of eight, which takes elements [64 w, 64 w + 64) of the stage.
-template <bool kFp4, bool kDown, int NT, int kNT, bool kLo>
-__device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT, kLo>& tok,
+template <bool kFp4, bool kDown, int NT, int kNT>
+__device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, const TokenFrags<kFp4, kNT>& tok,
                                               float (&acc)[Stage<kFp4>::kRowTiles][kNT][4], ErrorWord* ew) {
   using S = Stage<kFp4>;
   const int g = lane >> 2, t = lane & 3;
@@ -768,11 +768,6 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, c
         const uint4 b = tok.v[nt][kb];
         mma_16816<false>(acc[0][nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
         mma_16816<false>(acc[0][nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-        if constexpr (kLo) {
-          const uint4 r = tok.lo[nt][kb];
-          mma_16816<false>(acc[0][nt], lo.x, hi.x, lo.y, hi.y, r.x, r.y);
-          mma_16816<false>(acc[0][nt], lo.z, hi.z, lo.w, hi.w, r.z, r.w);
-        }
       }
     }
   } else {
@@ -816,6 +811,28 @@ __device__ __forceinline__ void consume_stage(uint32_t stage, int w, int lane, c
           acc[i][nt][3] = fmaf(part[3] * s1, f_hi, acc[i][nt][3]);
         }
       }
+    }
+  }
+}
+
+// As consume_stage for bf16, with two sets of token fragments: each weight fragment meets both.
+template <int kNT, typename Frags>
+__device__ __forceinline__ void consume_stage_two(uint32_t stage, int w, int lane, const Frags& first, const Frags& second,
+                                                  float (&acc)[kNT][4], float (&acc2)[kNT][4]) {
+  using S = Stage<false>;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t wr = stage + w * S::kColBytes + g * 128;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    const uint32_t at = wr + (((kb * 4 + t) ^ g) << 4);
+    const uint4 lo = lds128(at), hi = lds128(at + S::kBlock);
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const uint4 b = first.v[nt][kb], c = second.v[nt][kb];
+      mma_16816<false>(acc[nt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+      mma_16816<false>(acc[nt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+      mma_16816<false>(acc2[nt], lo.x, hi.x, lo.y, hi.y, c.x, c.y);
+      mma_16816<false>(acc2[nt], lo.z, hi.z, lo.w, hi.w, c.z, c.w);
     }
   }
 }
@@ -928,8 +945,7 @@ __device__ __forceinline__ void drain(Smem* sm, int stages, int grp, int lane) {
 // the kernel
 // ------------------------------------------------------------------------------------------------
 // kNT: column tiles of eight tokens (1 for batches of at most 8, whose fragments then take half the registers).
-// kTwoParts: h in two bf16 parts (bf16 experts).
-template <bool kFp4, int kNT, bool kTwoParts>
+template <bool kFp4, int kNT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     layer_decode_kernel(const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ CUtensorMap map_w3,
                         const __grid_constant__ CUtensorMap map_w2, const __grid_constant__ DecodeParams p) {
@@ -1009,9 +1025,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const float* scales[kFp4 ? kNT : 1][2];
       // Fragments of the next kSets stages, each set loaded again as soon as its stage is done.  Two where the
       // registers hold them: an L2 round trip under the stream is longer than a stage.
-      constexpr bool kLo = kDown && kTwoParts;
-      constexpr int kSets = kFp4 || (kLo && kNT == 2) ? 1 : 2;
-      TokenFrags<kFp4, kNT, kLo> frags[kSets];
+      constexpr int kSets = kFp4 ? 1 : 2;
+      TokenFrags<kFp4, kNT> frags[kSets];
+      // bf16 experts' h is held in two bf16 parts, 16 bits together.  The columns that an expert's few tokens leave
+      // free take the second parts: of up to 4 tokens in columns 4 to 7; of up to 8 tokens, with two column tiles,
+      // in the second.  More tokens need both sets of fragments for a stage: the other set holds the second
+      // parts (one column tile), or tokens 8 to 15 with theirs.  The sums of the two parts are kept apart and
+      // added at a tile's end: a token's result does not depend on how many others its expert has.
+      constexpr bool kParts = kDown && !kFp4;
+      int cols = 0;   // tokens of the tile entered
       int ready_a = -1;
       bool all_ready = !kDown;
       // Whether the iterator stands on a tile (waits for the lists at the first routed one).
@@ -1037,6 +1059,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         auto place = [&](int c) { return kDown ? r0 + c : sm->tok_of_row[r0 + c]; };
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
+          if constexpr (kParts) {   // one pointer: an expert's rows of h follow each other
+            const int col = n <= 4 ? g & 3 : g;
+            rows[0] = col < n ? base + (size_t)(r0 + col) * K + (n <= 4 && g >= 4 ? p.h_lo : 0) + w8 * 64 + t * 8 : nullptr;
+            cols = n;
+            break;
+          }
           rows[nt] = g + 8 * nt < n ? base + (size_t)place(g + 8 * nt) * K + w8 * 64 + t * 8 : nullptr;
           if constexpr (kFp4) {
             const float* sbase = kDown ? p.h_scale : p.x_scale;
@@ -1048,63 +1076,99 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
       };
-      auto fetch = [&](int s, TokenFrags<kFp4, kNT, kLo>& nxt) {   // those of stage s of the tile entered (zeros past its end)
+      // those of stage s of the tile entered (zeros past its end); h in parts: or its other set
+      auto fetch = [&](int s, TokenFrags<kFp4, kNT>& nxt, bool other = false) {
         const bool in = s * S::kChunk + w8 * 64 < K;
+        if constexpr (kParts) {
+          const uint16_t* at = rows[0] + s * S::kChunk;
+          if (other) at += kNT == 1 ? p.h_lo : 8 * K;
+          const bool have = in && rows[0] != nullptr && (kNT == 1 || !other || g + 8 < cols);
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          nxt.v[nt][0] = nxt.v[nt][1] = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (kLo) nxt.lo[nt][0] = nxt.lo[nt][1] = make_uint4(0u, 0u, 0u, 0u);
-          if (in && rows[nt] != nullptr) {
-            const uint4* at = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk);
+          for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)   // written during this kernel, except x itself: read from L2
-              nxt.v[nt][kb] = kDown || kFp4 ? __ldcg(at + kb * 4) : __ldg(at + kb * 4);
-            if constexpr (kLo) {
-              const uint4* lo = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk + p.h_lo);
+            for (int kb = 0; kb < 2; ++kb)   // written during this kernel: read from L2
+              nxt.v[nt][kb] = have && (nt == 0 || cols > 4)
+                                  ? __ldcg(reinterpret_cast<const uint4*>(at + (nt == 0 ? 0 : p.h_lo)) + kb * 4)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        } else {
 #pragma unroll
-              for (int kb = 0; kb < 2; ++kb) nxt.lo[nt][kb] = __ldcg(lo + kb * 4);
+          for (int nt = 0; nt < kNT; ++nt) {
+            nxt.v[nt][0] = nxt.v[nt][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (in && rows[nt] != nullptr) {
+              const uint4* at = reinterpret_cast<const uint4*>(rows[nt] + s * S::kChunk);
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb)   // written during this kernel, except x itself: read from L2
+                nxt.v[nt][kb] = kDown || kFp4 ? __ldcg(at + kb * 4) : __ldg(at + kb * 4);
+            }
+            if constexpr (kFp4) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                nxt.scale[nt][c] = in && scales[nt][c] != nullptr
+                                       ? __ldcg(reinterpret_cast<const float2*>(scales[nt][c] + s * (S::kChunk / 32)))
+                                       : make_float2(0.f, 0.f);
             }
           }
-          if constexpr (kFp4) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              nxt.scale[nt][c] = in && scales[nt][c] != nullptr
-                                     ? __ldcg(reinterpret_cast<const float2*>(scales[nt][c] + s * (S::kChunk / 32)))
-                                     : make_float2(0.f, 0.f);
-          }
         }
+      };
+      auto fetch_first = [&]() {
+        fetch(0, frags[0]);
+        const bool both = kParts && cols > 4 * kNT;
+        if (kSets == 2) fetch(both ? 0 : 1, frags[kSets - 1], both);
       };
       bool more = live();
       if (more) {
         enter();
-#pragma unroll
-        for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
+        fetch_first();
       }
       while (more) {
         const int n = sm->act_n[it.a], r0 = sm->act_off[it.a], a = it.a, blk = it.blk;
         float acc[S::kRowTiles][kNT][4] = {};
-        auto one_stage = [&](int s, TokenFrags<kFp4, kNT, kLo>& tok) {
+        auto one_stage = [&](int s, TokenFrags<kFp4, kNT>& tok) {
           stage_wait(&full[pos.slot], pos.phase, abort, p.ew, kDown ? 406 : 405);
           if (kFp4 || s * S::kChunk + w8 * 64 < K) {
             const uint32_t stage = ring_addr + pos.slot * S::kBytes;
-            if (kNT == 1 || n <= 8) consume_stage<kFp4, kDown, 1, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
-            else consume_stage<kFp4, kDown, kNT, kNT, kLo>(stage, w8, lane, tok, acc, p.ew);
+            if (kNT == 1 || n <= (kParts ? 4 : 8)) consume_stage<kFp4, kDown, 1, kNT>(stage, w8, lane, tok, acc, p.ew);
+            else consume_stage<kFp4, kDown, kNT, kNT>(stage, w8, lane, tok, acc, p.ew);
           }
           if (s + kSets < ns) fetch(s + kSets, tok);
           mbar_arrive_after_reads(&empty[pos.slot]);
           pos.step(1, p.stages);
         };
-        for (int s = 0; s < ns; s += kSets) {
-          one_stage(s, frags[0]);
-          if (kSets == 2 && s + 1 < ns) one_stage(s + 1, frags[kSets - 1]);
+        if (!kParts || n <= 4 * kNT) {
+          for (int s = 0; s < ns; s += kSets) {
+            one_stage(s, frags[0]);
+            if (kSets == 2 && s + 1 < ns) one_stage(s + 1, frags[kSets - 1]);
+          }
+          if constexpr (kParts) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[0][0][i] += n <= 4 ? __shfl_xor_sync(0xffffffffu, acc[0][0][i], 2) : acc[0][kNT - 1][i];
+          }
+        } else if constexpr (kParts) {
+          float acc2[kNT][4] = {};
+          for (int s = 0; s < ns; ++s) {
+            stage_wait(&full[pos.slot], pos.phase, abort, p.ew, 406);
+            if (s * S::kChunk + w8 * 64 < K)
+              consume_stage_two<kNT>(ring_addr + pos.slot * S::kBytes, w8, lane, frags[0], frags[kSets - 1], acc[0], acc2);
+            if (s + 1 < ns) {
+              fetch(s + 1, frags[0]);
+              fetch(s + 1, frags[kSets - 1], true);
+            }
+            mbar_arrive_after_reads(&empty[pos.slot]);
+            pos.step(1, p.stages);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[0][0][i] += kNT == 1 ? acc2[0][i] : acc[0][kNT - 1][i];
+            if (kNT == 2) acc[0][kNT - 1][i] = acc2[0][i] + acc2[kNT - 1][i];
+          }
         }
         // the next tile's first fragments are under way while this one is added up
         it.next();
         more = live();
         if (more) {
           enter();
-#pragma unroll
-          for (int q = 0; q < kSets; ++q) fetch(q, frags[q]);
+          fetch_first();
         }
         float* red = sm->red[grp][buf];
         if (kTwo) buf ^= 1;   // the barrier of the next tile keeps its writes behind this tile's reads
@@ -1132,11 +1196,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             } else {
               const __nv_bfloat16 v = __float2bfloat16_rn(h);
               *dst = *reinterpret_cast<const uint16_t*>(&v);
-              if constexpr (kTwoParts) {
-                const float rest = h - __bfloat162float(v);   // NaN for an infinite h, whose first part says enough
-                const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-                dst[p.h_lo] = *reinterpret_cast<const uint16_t*>(&lo);
-              }
+              const float rest = h - __bfloat162float(v);   // NaN for an infinite h, whose first part says enough
+              const __nv_bfloat16 lo = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+              dst[p.h_lo] = *reinterpret_cast<const uint16_t*>(&lo);
             }
           }
           // the router warps report the tile once all its writers are here
@@ -1219,14 +1281,8 @@ cudaError_t launch_layer_decode(const CUtensorMap& w1, const CUtensorMap& w3, co
   const size_t fixed = fp4 ? (p.T <= 8 ? sizeof(DecodeSmem<true, 1>) : sizeof(DecodeSmem<true, 2>))
                            : (p.T <= 8 ? sizeof(DecodeSmem<false, 1>) : sizeof(DecodeSmem<false, 2>));
   p.stages = (int)std::min<size_t>(kMaxStages, (smem - 1024 - fixed) / stage / kGroups);   // of each group's ring
-  // h rounded once to bf16, as everywhere in the library, puts about 0.7 of y's own rounding on top of it.  A
-  // second bf16 part (16 bits together) takes that away for a second MMA and fragment in the down projection:
-  // 142 us instead of 136 on the V3-shaped layer (T = 1), but nothing on small layers, which are bound by latency
-  // (18.4 us both ways at d = 256), so those take it: up to 32 MB of weights, 5 us of the stream.
-  const bool two = (long)(std::min(p.T * p.k, p.E) + 1) * p.d * p.I * 6 <= (32l << 20);
-  auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1, false> : layer_decode_kernel<true, 2, false>)
-                : two ? (p.T <= 8 ? layer_decode_kernel<false, 1, true> : layer_decode_kernel<false, 2, true>)
-                      : (p.T <= 8 ? layer_decode_kernel<false, 1, false> : layer_decode_kernel<false, 2, false>);
+  auto kernel = fp4 ? (p.T <= 8 ? layer_decode_kernel<true, 1> : layer_decode_kernel<true, 2>)
+                    : (p.T <= 8 ? layer_decode_kernel<false, 1> : layer_decode_kernel<false, 2>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // no more CTAs than any phase has work for: small layers pay for each arrival at the barriers

@@ -459,3 +459,43 @@ def test_decode_on_the_workspace_of_a_larger_batch(M, mxfp4):
     for T in (16, 1):
         part = dataclasses.replace(li, x=li.x[:T].contiguous())
         _check_gated(M, cfg.replace(T=T), part, w4, ws)
+
+
+# The precision of h, where y's own rounding does not hide it: features in pairs whose values are almost alike and
+# whose w2 columns are opposite, so that y is small beside what it is a sum of.  The roundings of h are independent
+# of each other, each below u |h| (u = 2^-16 for two bf16 parts, 2^-11 for f16; one bf16 would be off by 2^-9.3 in the
+# mean square), so in norm their sum is below u B, B^2 = sum_j w_j^2 (h_j^2 . (w2_j^T)^2) + h_s^2 . (w2_s^T)^2.  y is
+# rounded once more, 2^-8 |y|, and the fp32 sums and the fast exponential leave 2^-17 A as a worst case: sums of up
+# to 2^6 additions a lane, truncated by up to 2^-23 each.
+@pytest.mark.parametrize("mxfp4", [False, True])
+@pytest.mark.parametrize("T,dim,inter", [(1, 512, 512), (3, 1024, 512), (7, 512, 1024), (16, 512, 512), (1, 2048, 2048), (6, 2048, 2048),
+                                         (16, 2048, 2048)])
+def test_decode_holds_h_to_more_than_bf16(M, T, dim, inter, mxfp4):
+    cfg = TINY.replace(T=T, dim=dim, inter_dim=inter)
+    li, w4 = _layer(cfg, mxfp4)
+    if mxfp4:
+        for name in ("w1", "w1s", "w3", "w3s"):
+            t = getattr(w4, name)
+            t[:, 1::2] = t[:, 0::2]
+        w4.w3[:, 1::2, 5] ^= 1                                  # one code of the row
+        w4.w2.copy_((w4.w2 & 0x0f) | ((w4.w2 & 0x0f) << 4) ^ 0x80)   # the second code of a byte: the first's opposite
+    else:
+        li.w1[:, 1::2] = li.w1[:, 0::2]
+        li.w3[:, 1::2] = li.w3[:, 0::2] * (1 + 2.0 ** -6)
+        li.w2[:, :, 1::2] = -li.w2[:, :, 0::2]
+    y, w, idx, cnt, ws = _decode(M, cfg, li, w4)
+    M.check_device_errors(ws, "moe_decode")
+    ref, A, _ = _reference(cfg, li, w4, idx, w.double())
+    B2 = torch.zeros_like(ref)
+    x = li.x.double()
+    for e in sorted({e for row in idx.tolist() for e in row} | {cfg.n_experts}):
+        w1, w3, w2 = _weights64(li, w4, e)
+        scale = torch.tensor([1.0 if e == cfg.n_experts else sum(float(w[t, j]) for j in range(cfg.topk) if idx[t, j] == e)
+                              for t in range(T)], dtype=torch.float64, device="cuda")[:, None]
+        g = x @ w1.t()
+        B2 += scale ** 2 * ((g * torch.sigmoid(g) * (x @ w3.t())) ** 2 @ (w2 ** 2).t())
+    u = 2.0 ** -11 if mxfp4 else 2.0 ** -16
+    err = float((y.double() - ref).norm())
+    lim = u * float(B2.sqrt().norm()) + 2.0 ** -8 * float(ref.norm()) + 2.0 ** -17 * float(A.norm())
+    assert lim < 2.0 ** -10 * float(B2.sqrt().norm())    # else the case would not tell
+    assert err <= lim, err / lim
