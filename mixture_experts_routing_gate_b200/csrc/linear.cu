@@ -22,13 +22,15 @@ namespace {
 // the epilogue
 // ------------------------------------------------------------------------------------------------
 // NaN goes through every branch.  silu and the tanh form of gelu are z / (1 + e^-a) (no cancellation for
-// negative z); the exact gelu uses erfc for the same reason.
-template <int kAct>
+// negative z); the exact gelu uses erfc for the same reason.  The fast exponential's error grows with its argument (2^-20
+// at z = -10), far below a bf16 output's rounding, not below an fp32 one's: kExact takes the accurate one.
+template <int kAct, bool kExact>
 __device__ __forceinline__ float activate(float z) {
+  auto e = [](float a) { return kExact ? expf(a) : __expf(a); };
   if (kAct == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (kAct == MOE_ACT_SILU) return __fdiv_rn(z, 1.f + __expf(-z));
+  if (kAct == MOE_ACT_SILU) return __fdiv_rn(z, 1.f + e(-z));
   if (kAct == MOE_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
-  if (kAct == MOE_ACT_GELU_TANH) return __fdiv_rn(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+  if (kAct == MOE_ACT_GELU_TANH) return __fdiv_rn(z, 1.f + e(-1.5957691f * (z + 0.044715f * z * z * z)));
   return z;
 }
 
@@ -52,12 +54,12 @@ __device__ __forceinline__ uint4 load_residual8(const LinearParams& p, int t, lo
   return *reinterpret_cast<const uint4*>(p.residual + (size_t)t * p.ldr + c);
 }
 
-template <int kAct>
+template <int kAct, bool kExact>
 __device__ __forceinline__ void finish8(const LinearParams& p, int t, long c, const float (&z)[8], const float (&bias)[8],
                                         const uint4& res) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate<kAct>(z[i] + bias[i]);
+  for (int i = 0; i < 8; ++i) v[i] = activate<kAct, kExact>(z[i] + bias[i]);
   const bool whole = whole8(p, c);
   if (p.residual != nullptr) {
     if (whole && p.residual_vec) {
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         float b[8];
         load_bias8(p, c8, b);
         const uint4 res = load_residual8(p, col, c8);
-        with_activation(p.act, [&](auto act) { finish8<decltype(act)::value>(p, col, c8, z, b, res); });
+        with_activation(p.act, [&](auto act) { finish8<decltype(act)::value, true>(p, col, c8, z, b, res); });
       }
       u = end;
     }
@@ -393,7 +395,7 @@ __device__ __forceinline__ LinUnit lin_unit(const LinearParams& p, int w) {
   return u;
 }
 
-// kPromote (fp32 outputs): the tensor cores add into the fp32 accumulator with truncation, a bias that grows
+// kPromote (fp32 outputs; bf16 ones round 2^-8, five hundred times as much): the tensor cores add into the fp32 accumulator with truncation, a bias that grows
 // with the number of steps -- 8e-6 of the result after 7168 products.  So K is accumulated in chunks of
 // kPromoteSteps * 64, alternating between the two accumulators, and the epilogue warps add the chunks in
 // registers, rounding to nearest.
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const float4* src = reinterpret_cast<const float4*>(stage + r * kEpiPitch + (lane & 3) * 8);
             const float4 lo = src[0], hi = src[1];
             const float z[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            if (in && row0 + r < p.T) finish8<decltype(act)::value>(p, row0 + r, c8, z, b8, res[i]);
+            if (in && row0 + r < p.T) finish8<decltype(act)::value, kPromote>(p, row0 + r, c8, z, b8, res[i]);
           }
           __syncwarp();
         }
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             z[0] += lo.x; z[1] += lo.y; z[2] += lo.z; z[3] += lo.w;
             z[4] += hi.x; z[5] += hi.y; z[6] += hi.z; z[7] += hi.w;
           }
-          finish8<decltype(act)::value>(p, t, c8, z, b8, res);
+          finish8<decltype(act)::value, kPromote>(p, t, c8, z, b8, res);
         }
       });
     }

@@ -307,3 +307,45 @@ def test_small_batches_on_the_workspace_of_a_large_one(M):
         M.moe_linear(desc, x, w, y, ws)
         M.check_device_errors(ws)
         _check(y, x, w, "none", None, None)
+
+
+@pytest.mark.parametrize("T", [1, 9, 40, 300, 5000])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_fp32_outputs_take_the_accurate_exponential(M, T, act):
+    # one-hot rows, so that z is exact: what remains is the activation.  expf is good to 2^-23, the sum and the
+    # division round 2^-24 each: 2^-22.  gelu_tanh's exponent a has seven roundings of 2^-24 (no cancellation), which
+    # e^a turns into 7 |a| 2^-24.  Where e^a passes fp32's range, 2^128, z / (1 + e^a) is zero instead of less than
+    # |z| 2^-128 (a = 88.7 at z = -10.1, where that is 2.5 times the smallest normal number, 2^-126).
+    K, N = 8, 512
+    w = torch.zeros((N, K), dtype=torch.bfloat16, device="cuda")
+    w[:, 3] = torch.linspace(-30.0, 30.0, N, device="cuda").to(torch.bfloat16)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    x[:, 3] = 1.0
+    desc = M.linear_desc(K, N, act, torch.float32)
+    y = torch.empty((T, N), dtype=torch.float32, device="cuda")
+    M.moe_linear(desc, x, w, y, M.LinearWorkspace(desc, T))
+    z = w[:, 3].double().expand(T, N)
+    want = _act64(z, act)
+    a = torch.zeros_like(z) if act == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    lim = (2.0 ** -22 + 7 * a.abs() * 2.0 ** -24) * want.abs() + 2.0 ** -126 + z.abs() * 2.0 ** -128
+    assert bool(((y.double() - want).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 300])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_infinity_goes_through_as_in_the_formula(M, T, out):
+    # an infinite product stays in its row; ReLU clears the negative one
+    K, N = 64, 136
+    x, w = _normal((T, K), 1.0, 3), _normal((N, K), 1.0, 4)
+    want, y = (torch.empty((T, N), dtype=out, device="cuda") for _ in range(2))
+    for act in ("none", "relu"):
+        desc = M.linear_desc(K, N, act, out)
+        ws = M.LinearWorkspace(desc, T)
+        clean = x.clone()
+        M.moe_linear(desc, clean, w, want, ws)
+        clean[0, 7] = float("inf")
+        M.moe_linear(desc, clean, w, y, ws)
+        assert torch.equal(y[1:], want[1:])
+        s = torch.sign(w[:, 7].float())
+        first = torch.where(s > 0, float("inf"), 0.0 if act == "relu" else float("-inf"))
+        assert torch.equal(y[0].float()[s != 0], first[s != 0]) and bool(y[0].isnan()[s == 0].all())
