@@ -326,7 +326,8 @@ moe_status moe_forward(const moe_layer_desc* desc, int T, const moe_bf16* x, con
  * As in moe_forward, a hash-routed call uses neither bias nor logit_offset.
  * The selection may differ from moe_forward's where two experts' scores agree to fp32 rounding.
  * A table row that names an expert twice counts it twice (in the weights, in y and in counts_out).
- * desc->options, token_chunk and gate_prepared choose nothing here (they are still checked).
+ * desc->options, token_chunk and gate_prepared choose nothing here (they are still checked); dim and inter_dim
+ * go up to 2^21 (MOE_ERR_UNSUPPORTED above).
  * The launch is cooperative: it starts when every SM it uses has room for its CTA, and it can be
  * captured in a CUDA graph.  The workspace (moe_workspace_bytes(desc, T), initialised once) holds the
  * grid's counters and rows, so calls that may run at the same time need a workspace each.
@@ -427,7 +428,7 @@ moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x
  * y (out): T rows of N bf16, or fp32 when out_fp32 is 1, at stride ldy.  Strides are in elements.
  * y may be the residual itself (bf16, the same pointer and stride); it must not overlap x, w or bias.
  * What lies between the rows of y (ldy > N) is left as it was.
- * Needs K % 8 == 0 and ldx % 8 == 0 (MOE_ERR_UNSUPPORTED otherwise); x and w 16-byte aligned, the others
+ * Needs K % 8 == 0 and ldx % 8 == 0, T, K and N up to 2^30 (MOE_ERR_UNSUPPORTED otherwise); x and w 16-byte aligned, the others
  * aligned to their elements, ldx >= K, ldy >= N, ldr >= N (MOE_ERR_INVALID otherwise).
  * ws: moe_linear_workspace_bytes(desc, T) bytes, 1 KiB aligned, cleared once by moe_workspace_init; a
  * workspace serves one call at a time, and any descriptor it is large enough for; one for T tokens serves

@@ -869,6 +869,8 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   const bool hashed = token_ids != nullptr || tid2eid != nullptr;
   if (T < 0) return MOE_ERR_INVALID;
   if (T > MOE_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  // rows of the stacked weights, (n_experts + 1) dim or inter_dim of them, are numbered in 32 bits
+  if (std::max(desc->dim, desc->inter_dim) > (1 << 21)) return MOE_ERR_UNSUPPORTED;
   if (hashed && (token_ids == nullptr || tid2eid == nullptr || vocab <= 0)) return MOE_ERR_INVALID;
   if (hashed && desc->score_func == MOE_SCORE_SOFTMAX) return MOE_ERR_UNSUPPORTED;
   if (fp4 != nullptr) {
@@ -927,11 +929,14 @@ moe_status decode_impl(const moe_layer_desc* desc, int T, const moe_bf16* x, con
   return cuda_status(moe::launch_layer_decode(m1, m3, m2, p, fp4 != nullptr, num_sms(), s));
 }
 
+constexpr int kLinearMaxSize = 1 << 30;
 moe_status check_linear(const moe_linear_desc* d, int T) {
   if (d == nullptr || T < 0 || d->in_features <= 0 || d->out_features <= 0) return MOE_ERR_INVALID;
   if (d->activation < MOE_ACT_NONE || d->activation > MOE_ACT_GELU_TANH || (d->out_fp32 != 0 && d->out_fp32 != 1))
     return MOE_ERR_INVALID;
   if (d->in_features % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  // rows and features are rounded up to tiles in 32 bits
+  if (std::max({T, d->in_features, d->out_features}) > kLinearMaxSize) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -439,3 +439,20 @@ def test_linear_workspace_for_a_batch_serves_every_smaller_one(moe, K, N):
     d = moe.linear_desc(K, N)
     sizes = [moe.moe_linear_workspace_bytes(d, T) for T in [*range(400), 1024, 4096, 16384]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_sizes_beyond_the_kernels_index_arithmetic_are_refused(moe):
+    P = ctypes.c_void_p
+    fake = P(1 << 20)   # never dereferenced: every call must fail its checks first
+    big = (1 << 31) - 8
+
+    def linear(T, K, N):
+        d = moe.linear_desc(K, N)
+        assert moe.moe_linear_workspace_bytes(d, T) == 0
+        return moe.lib.moe_linear(ctypes.byref(d), T, fake, K, fake, None, None, 0, fake, N, fake, 1 << 40, None)
+
+    assert linear(1, 8, big) == linear(1, big, 8) == linear(big, 8, 8) == moe.MOE_ERR_UNSUPPORTED
+    for sizes in (dict(dim=1 << 22), dict(inter_dim=1 << 22)):
+        d = moe.layer_desc(W.CONFIGS["tiny"].replace(**sizes))
+        assert moe.lib.moe_decode(ctypes.byref(d), 1, fake, None, None, 0, fake, None, None, fake, fake, fake, fake, None, None,
+                                  None, fake, 1 << 60, None) == moe.MOE_ERR_UNSUPPORTED
