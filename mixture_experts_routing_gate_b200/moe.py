@@ -424,6 +424,12 @@ def _shape(t: Optional[torch.Tensor], dtype, shape, name: str, device: int):
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
+def _space(ws: Workspace, device: int):
+    """The few-token layer and the linear projection run where their workspace is."""
+    if ws.tensor.get_device() != device:
+        raise ValueError(f"the workspace is on {ws.tensor.device}, the current device is cuda:{device}")
+
+
 def _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
                    dev):
     T, d, E, k = x.shape[0], desc.dim, desc.n_experts, desc.topk
@@ -449,6 +455,7 @@ def moe_decode(desc, x, w_gate, w1, w3, w2, y, ws: Workspace, bias=None, logit_o
                tid2eid=None, weights_out=None, indices_out=None, counts_out=None, stream=None):
     """moe_forward for at most MOE_DECODE_MAX_TOKENS tokens in one kernel launch."""
     dev = torch.cuda.current_device()
+    _space(ws, dev)
     T = _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
                        dev)
     E1, d, I = desc.n_experts + 1, desc.dim, desc.inter_dim
@@ -466,6 +473,7 @@ def moe_decode_mxfp4(desc, x, w_gate, w, y, ws: Workspace, bias=None, logit_offs
                      tid2eid=None, weights_out=None, indices_out=None, counts_out=None, stream=None):
     """moe_decode with MXFP4 expert weights ``w`` (see mxfp4_weights) and bf16 activations."""
     dev = torch.cuda.current_device()
+    _space(ws, dev)
     T = _decode_shapes(desc, x, w_gate, y, bias, logit_offset, token_ids, tid2eid, weights_out, indices_out, counts_out,
                        dev)
     E1, d, I = desc.n_experts + 1, desc.dim, desc.inter_dim
@@ -493,6 +501,7 @@ def moe_linear(desc: LinearDesc, x, w, y, ws: LinearWorkspace, bias=None, residu
     """y = act(x w^T + bias) + residual.  x [T, K], y and residual [T, N] may be rows of wider tensors; y may be
     residual itself."""
     dev = torch.cuda.current_device()
+    _space(ws, dev)
     T, K, N = x.shape[0], desc.in_features, desc.out_features
     ldx = _rows(x, torch.bfloat16, T, K, "x", dev)
     ldy = _rows(y, torch.float32 if desc.out_fp32 else torch.bfloat16, T, N, "y", dev)

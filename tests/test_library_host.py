@@ -456,3 +456,17 @@ def test_sizes_beyond_the_kernels_index_arithmetic_are_refused(moe):
         d = moe.layer_desc(W.CONFIGS["tiny"].replace(**sizes))
         assert moe.lib.moe_decode(ctypes.byref(d), 1, fake, None, None, 0, fake, None, None, fake, fake, fake, fake, None, None,
                                   None, fake, 1 << 60, None) == moe.MOE_ERR_UNSUPPORTED
+
+
+def test_workspace_on_another_device_is_refused(moe, monkeypatch):
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ws = types.SimpleNamespace(tensor=torch.empty(8192, dtype=torch.uint8), ptr=0, nbytes=8192)   # host memory: device -1
+    d, t = moe.layer_desc(W.CONFIGS["tiny"]), torch.empty(0)
+    calls = (lambda: moe.moe_decode(d, t, t, t, t, t, t, ws), lambda: moe.moe_decode_mxfp4(d, t, t, None, t, ws),
+             lambda: moe.moe_linear(moe.linear_desc(64, 32), t, t, t, ws))
+    for call in calls:
+        with pytest.raises(ValueError, match="workspace"):
+            call()
