@@ -499,3 +499,75 @@ def test_decode_holds_h_to_more_than_bf16(M, T, dim, inter, mxfp4):
     lim = u * float(B2.sqrt().norm()) + 2.0 ** -8 * float(ref.norm()) + 2.0 ** -17 * float(A.norm())
     assert lim < 2.0 ** -10 * float(B2.sqrt().norm())    # else the case would not tell
     assert err <= lim, err / lim
+
+
+def test_decode_mxfp4_spread_inside_a_block_of_x(M):
+    # x in f16 blocks of 32 is exact down to 2^-31 of the block's largest value; a value of that size is all that the
+    # weights see of its block here (the largest one meets zero codes)
+    cfg = TINY.replace(T=2, dim=512, inter_dim=512, n_groups=1, n_limited_groups=1, topk=1)
+    li, w4 = _layer(cfg, mxfp4=True)
+    li.x[:] = 0
+    li.x[:, 64] = 1.0
+    li.x[0, 65], li.x[1, 95] = 2.0 ** -31 * (255 / 128), -2.0 ** -31
+    for name in ("w1", "w3"):
+        getattr(w4, name)[:] = 0
+        getattr(w4, name)[:, :, 32] = 0x70      # column 65: 6
+        getattr(w4, name)[:, :, 47] = 0x50      # column 95: 3
+        getattr(w4, name + "s").fill_(127 + 25)
+    _check_gated(M, cfg, li, w4)
+
+
+def test_decode_mxfp4_scales_of_the_up_projections(M):
+    # w1's and w3's scales over 200 powers of two, opposite to each other so that h stays in range
+    cfg = TINY.replace(T=3, dim=512, inter_dim=1024, n_groups=1, n_limited_groups=1, topk=2)
+    li, w4 = _layer(cfg, mxfp4=True)
+    r = (torch.arange(cfg.inter_dim, device="cuda") // 32 * 7 % 200 - 100)[None, :, None]
+    w4.w1s[:] = (127 + r).to(torch.uint8)
+    w4.w3s[:] = (127 - r).to(torch.uint8)
+    _check_gated(M, cfg, li, w4)
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
+def test_decode_infinity_and_nan_stay_in_their_token(M, mxfp4):
+    # every expert for every token, so that routing (and with it the order of sums) cannot differ
+    cfg = TINY.replace(T=5, dim=512, inter_dim=512, n_groups=1, n_limited_groups=1, topk=4, bias_std=None)
+    li, w4 = _layer(cfg, mxfp4)
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None].contiguous()
+    ids = torch.zeros(5, dtype=torch.int32, device="cuda")
+    want = _decode(M, cfg, li, w4, table=table, ids=ids)[0]
+    li.x[1, 40], li.x[3, 500] = float("inf"), float("nan")
+    y, _, _, _, ws = _decode(M, cfg, li, w4, table=table, ids=ids)
+    M.check_device_errors(ws)
+    for t in (0, 2, 4):
+        assert torch.equal(y[t], want[t])
+    assert not bool(torch.isfinite(y[1]).any()) and bool(torch.isnan(y[3]).all())
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+def test_decode_with_experts_switched_off_by_their_bias(M, groups):
+    cfg = TINY.replace(T=16, n_groups=groups, n_limited_groups=min(groups, 2), topk=3)
+    li, _ = _layer(cfg)
+    off = torch.tensor([0, 5, 6, 9, 15], device="cuda")
+    li.bias[off] = float("-inf")
+    y, w, idx, cnt, ws = _decode(M, cfg, li, None)
+    assert not bool(torch.isin(idx, off.to(torch.int32)).any())
+    _check(M, cfg, li, None, y, w, idx, cnt, ws)
+    if groups == 1:      # as with a bias below every other
+        li.bias[off] = -1e4
+        again = _decode(M, cfg, li, None)
+        assert torch.equal(again[2], idx) and torch.equal(again[0], y)
+
+
+def test_decode_results_do_not_depend_on_the_batch(M):
+    # one token alone, among 7 and among 16 on the same experts: the same bits, whichever columns h's parts take
+    import dataclasses
+    cfg = TINY.replace(T=16, dim=512, inter_dim=1024, n_groups=1, n_limited_groups=1, topk=4, bias_std=None)
+    li, _ = _layer(cfg)
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None].contiguous()
+    ys = []
+    for T in (16, 8, 7, 4, 2, 1):
+        part = dataclasses.replace(li, x=li.x[:T].contiguous())
+        ys.append(_decode(M, cfg.replace(T=T), part, None, table=table, ids=torch.zeros(T, dtype=torch.int32, device="cuda"))[0])
+    for y in ys:
+        assert torch.equal(y[:1], ys[0][:1])
+        assert torch.equal(y, ys[0][:len(y)])
