@@ -407,7 +407,8 @@ moe_status moe_forward_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* 
  * moe_decode with MXFP4 expert weights (as for moe_expert_ffn_mxfp4: dim % 512 == 0, inter_dim % 512
  * == 0).  The weights are used exactly.  The activations keep the precision of bf16 whether
  * MOE_OPT_MXFP4_BF16_ACTIVATIONS is set or not: x and h are held in f16 in blocks of 32 elements with a
- * power-of-two scale each, exact for values of x down to 2^-32 of their block's largest, h rounded once (2^-12).
+ * power-of-two scale each, exact for values of x down to 2^-31 of their block's largest (off by at
+ * most 2^-39 of it below), h rounded once (2^-11).
  */
 moe_status moe_decode_mxfp4(const moe_layer_desc* desc, int T, const moe_bf16* x,
                             const int32_t* token_ids, const int32_t* tid2eid, int vocab,

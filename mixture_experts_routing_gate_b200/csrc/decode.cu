@@ -7,7 +7,7 @@
 // far below the flops per byte at which the tensor cores would matter.  So the kernel is a weight stream:
 //
 // * one CTA per SM, all resident at once (cooperative launch).  Two producer warps keep TMA copies of 8 KB in
-//   flight into two rings of together 110 to 190 KB of shared memory, two groups of eight consumer warps
+//   flight into two rings of together 136 (MXFP4) or 160 KB of shared memory, two groups of eight consumer warps
 //   compute, each on tiles of its own.  At 44 bytes/ns per SM the rings hold about 4 us of the stream, more
 //   than the memory latency, so the stream does not stop between the phases.  (Copies of single rows, 1 KB,
 //   cost about 65 ns each whoever issues them and held the stream at 2 TB/s.)
@@ -36,8 +36,8 @@
 // hardware's E2M1 -> f16 conversion takes 73 codes/clock/SM (measured; the stream brings 44), where placing
 // the bits by shifts and logic, 15 operations for 8 codes, takes 34 and bounded the first form of this kernel
 // at 1.4 TB/s.  So the MMAs are f16: the activations of each block of 32 are scaled by a power of two to below
-// 2^15 and held in f16 (exact for bf16 values down to 2^-32 of the block's largest, off by 2^-40 of it
-// below), and the block's scale and the weights' UE8M0 scale multiply the fp32 accumulators of its 32
+// 2^15 and held in f16 (exact for bf16 values down to 2^-31 of the block's largest, off by 2^-39 of it
+// at most below), and the block's scale and the weights' UE8M0 scale multiply the fp32 accumulators of its 32
 // elements.  An up tile is 32 features, one block of h, whose scale its epilogue can therefore choose; tiles
 // are 64 rows, 512 codes of k a stage, so a token fragment serves four MMA row tiles.  Measured: d = 7168, I =
 // 2048, one token 74 us (33), eight tokens 350 us (206); half of the issue slots are used, so what is left is in
@@ -193,26 +193,6 @@ __device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, volat
   __syncwarp();
 }
 
-template <bool kF16>
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  if (kF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -1022,7 +1002,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       constexpr bool kDown = decltype(down_tag)::value, kTwo = S::red_bufs(kNT) == 2;
       const int K = kDown ? p.I : p.d, ns = (K + S::kChunk - 1) / S::kChunk;
       const uint16_t* rows[kNT];               // the tile's token rows, bf16 or (MXFP4) f16, at this warp's part
-      const float* scales[kFp4 ? kNT : 1][2];
+      [[maybe_unused]] const float* scales[kFp4 ? kNT : 1][2];
       // Fragments of the next kSets stages, each set loaded again as soon as its stage is done.  Two where the
       // registers hold them: an L2 round trip under the stream is longer than a stage.
       constexpr int kSets = kFp4 ? 1 : 2;

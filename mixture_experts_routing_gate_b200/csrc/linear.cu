@@ -146,19 +146,6 @@ __device__ __forceinline__ void stream_sync() {   // the consumer warps, whole
 }
 static_assert(kStreamConsumers == 512, "the named barrier's thread count");
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-
 // First stage of CTA c of G, and the CTA that has stage u, of U stages dealt in equal runs.
 // (A stage is 16 KB of weights, so their number fits an int.)
 __device__ __forceinline__ int run_start(int U, int c, int G) { return (int)((long)U * c / G); }
@@ -248,8 +235,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           const uint4 lo = lds128(at + i * 16 * 128), hi = lds128(at + (i * 16 + 8) * 128);
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
-            mma_16816(acc[i][nt], lo.x, hi.x, lo.y, hi.y, cur[nt].x, cur[nt].y);
-            mma_16816(acc[i][nt], lo.z, hi.z, lo.w, hi.w, cur[nt].z, cur[nt].w);
+            mma_16816<false>(acc[i][nt], lo.x, hi.x, lo.y, hi.y, cur[nt].x, cur[nt].y);
+            mma_16816<false>(acc[i][nt], lo.z, hi.z, lo.w, hi.w, cur[nt].z, cur[nt].w);
           }
         }
         mbar_arrive_after_reads(&sm->empty[slot]);
