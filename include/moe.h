@@ -319,7 +319,9 @@ moe_status moe_forward(const moe_layer_desc* desc, int T, const moe_bf16* x, con
  * MoE.forward for a few tokens: the arguments, outputs and definitions of moe_forward, computed by one
  * kernel launch for T <= MOE_DECODE_MAX_TOKENS (MOE_ERR_UNSUPPORTED above).  Made for decode batches,
  * where moe_forward's seven launches and their gaps cost more than the arithmetic: the whole grid is
- * resident and streams the chosen experts' weights without a break from the gate to the combine.
+ * resident and streams the chosen experts' weights without a break from the gate to the combine.  (It is the
+ * faster call up to 8 tokens; at 16 the two are level, and moe_forward is ahead where about a hundred experts
+ * are active.)
  * Values: the same formulas with fp32 accumulation; unlike in moe_forward, h is held in two bf16 parts (off by at
  * most 2^-16 of itself) and the expert outputs stay in fp32 until the combine.  Results do not depend on
  * scheduling, nor a token's on the other tokens of its batch beyond the order of fp32 sums.

@@ -40,7 +40,7 @@
 // at most below), and the block's scale and the weights' UE8M0 scale multiply the fp32 accumulators of its 32
 // elements.  An up tile is 32 features, one block of h, whose scale its epilogue can therefore choose; tiles
 // are 64 rows, 512 codes of k a stage, so a token fragment serves four MMA row tiles.  Measured: d = 7168, I =
-// 2048, one token 74 us (33), eight tokens 350 us (206); half of the issue slots are used, so what is left is in
+// 2048, one token 75 to 79 us (33), eight tokens 350 to 362 us (206); half of the issue slots are used, so what is left is in
 // the consumers' instructions and waits.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

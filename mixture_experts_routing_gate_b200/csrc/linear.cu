@@ -116,7 +116,7 @@ __device__ __forceinline__ void with_activation(int act, F&& f) {
 //
 // Work is cut into stages of 64 weight rows x 128 elements of k (16 KB), numbered tile by tile, and every
 // CTA takes an equal run of them, whatever the number of tiles: 112 tiles of 64 rows on 148 SMs would keep a
-// quarter of them idle.  (7168 x 7168, one token: 20 us in a graph, of which the weights' bytes need 16.)  A tile that spans several CTAs is added up by the last of them to arrive, from
+// quarter of them idle.  (7168 x 7168, one token: 21 us in a graph, of which the weights' bytes need 16.)  A tile that spans several CTAs is added up by the last of them to arrive, from
 // fp32 partials in the workspace and in the order of the CTAs, so results do not depend on scheduling
 // and no CTA waits for another.
 //
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // consecutive features of a row and stores 16 bytes; what it reads (bias, residual) is loaded before the
 // block's accumulators are, since its latency, not its arithmetic, bounded the tile.
 //
-// Measured: 16384 x 5120 x 5120 1.20 to 1.25 PFLOP/s, 0.87 to 0.91 of cuBLAS's sustained rate; the loads are then
-// 9.8 TB/s from L2 to all SMs, which bounds it.  64 x 7168 onto 129280 fp32 logits 341 to 368 us (288 at the
+// Measured: 16384 x 5120 x 5120 1.15 to 1.25 PFLOP/s, 0.83 to 0.91 of cuBLAS's sustained rate; the loads are then
+// 9 to 9.8 TB/s from L2 to all SMs, which bounds it.  64 x 7168 onto 129280 fp32 logits 341 to 406 us (288 at the
 // measured bandwidth).
 //
 // splits > 1 (fewer tiles than SMs; single CTAs): K is cut over a cluster of 2, 4 or 8 CTAs.  Each leaves its
